@@ -278,6 +278,117 @@ int mla_head_gemm(const void *x, int64_t ldx, int64_t x_head_stride, const void 
                   int64_t y_head_stride, int m, int n, int k, int heads, void *stream);
 
 /*
+ * Decode attention for a batch whose sequences begin with the same cached prefix (a system prompt, a
+ * document): the prefix blocks are held once, are read once per 128 query rows of the whole batch
+ * instead of once per sequence, and the heads of several sequences fill the tensor tiles together. The
+ * pages have no counterpart. The result is that of mla_decode with block tables that all begin with
+ * shared_table: token j of sequence b lies in block shared_table[j / 64] for j < 64 * shared_blocks and in
+ * block_table[b * bt_stride + j / 64] behind that.
+ *   shared_table   int32[shared_blocks]         physical blocks of the prefix (whole blocks of 64 tokens, as
+ *                  a paged cache shares them); NULL with shared_blocks = 0 (no prefix: a plain decode)
+ *   block_table    int32[batch, bt_stride]      entries [shared_blocks, ceil(n_b/64)) of row b are read, the
+ *                  first shared_blocks ones never
+ *   seqlens        int32[batch]                 tokens of each sequence, the prefix included; one that ends
+ *                  inside the prefix (or is empty) sees its first n_b tokens of it
+ *   tile_meta, num_splits, num_parts: from mla_get_metadata_shared for these seqlens, batch, s_q, h_q and
+ *                  shared_blocks; num_splits has mla_shared_units(...) + 1 entries
+ *   workspace      >= mla_shared_workspace_bytes(batch, s_q, h_q, shared_blocks, num_parts) bytes,
+ *                  256-aligned; contents on entry are ignored. Calls that may overlap need one each.
+ * All other arguments, outputs and status rules are those of mla_decode. Cache rows that some query row
+ * sees must be finite; rows past every sequence's end may hold anything.
+ * Precision: scores, softmax sums and outputs are accumulated in fp32 and the probabilities rounded to
+ * bf16 (to nearest) for the second product, so that an output is off by at most 2^-8 (half a bf16 step) of
+ * sum_j p_j |k_j| besides its own rounding; lse does not see that rounding. There is no range limit as in
+ * mla_decode. Results do not depend on timing: no atomics, a fixed order of sums for given metadata.
+ * Two launches on `stream`; allocates nothing.
+ */
+int64_t mla_shared_units(int batch, int s_q, int h_q, int shared_blocks);  /* 0 for invalid sizes; host only */
+/* Default start-up cost of a unit for mla_get_metadata_shared, in tiles of 128 tokens. Host only. */
+int mla_shared_fixed_cost(void);
+/* Bytes of workspace mla_decode_shared needs (0 for invalid sizes). Host only. */
+size_t mla_shared_workspace_bytes(int batch, int s_q, int h_q, int shared_blocks, int num_parts);
+/* The schedule: mla_get_metadata's rule over the work units of mla_decode_shared, in tiles of 128 tokens.
+ * Units: if s_q * h_q is no multiple of 128 (and shared_blocks > 0), ceil(batch * s_q * h_q / 128) row tiles
+ * of the batch over the prefix blocks, then ceil(s_q * h_q / 128) row tiles of each sequence over its own
+ * blocks; otherwise only the latter, over prefix and own blocks alike. Field 5 of a part holds the number
+ * of prefix tokens that the longest sequence reaches. One single-CTA launch. */
+int mla_get_metadata_shared(const int32_t *seqlens, int batch, int s_q, int h_q, int shared_blocks, int num_parts,
+                            int fixed_cost, int32_t *tile_meta, int32_t *num_splits, void *stream);
+int mla_decode_shared(const void *q, const void *kv_cache, int64_t num_blocks, const int32_t *shared_table,
+                      int shared_blocks, const int32_t *block_table, int64_t bt_stride, const int32_t *seqlens,
+                      const int32_t *tile_meta, const int32_t *num_splits, int num_parts, int batch, int s_q, int h_q,
+                      float scale, int causal, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * Rotary positions of the 64 rotary dims. Pair i (interleaved = 1: dims 2i and 2i + 1; 0: dims i and
+ * i + 32) at position p is turned by p * f_i and multiplied by `magnitude`:
+ *     y0 = magnitude * (x0 cos - x1 sin),  y1 = magnitude * (x0 sin + x1 cos)
+ * mla_rope_init fills a mla_rope on the host (no device work): f_i = base^(-2i/64) for factor = 1. For
+ * factor > 1 (a context scaled to factor times its original length) f_i is interpolated: with original_len
+ * = 0 every f_i is divided by factor; otherwise piecewise ("YaRN: Efficient Context Window Extension of
+ * Large Language Models", section 3.2): pairs that make at least beta_fast turns over original_len positions
+ * keep f_i, pairs with at most beta_slow turns take f_i / factor, with a linear ramp over i between.
+ * `magnitude` is the caller's (1, or the scaled model's factor on queries and keys).
+ *   turns[i] = round(2^64 * f_i / (2 pi)): the angle of position p is the fraction p * turns[i] mod 2^64 of
+ *   a full turn, so every int32 position is reduced exactly.
+ * Returns MLA_ERR_INVALID_ARG unless base > 1, factor >= 1, original_len >= 0, beta_fast >= beta_slow > 0
+ * and all are finite.
+ */
+typedef struct mla_rope {
+    uint64_t turns[32];
+    float magnitude;
+    int32_t interleaved;
+} mla_rope;
+int mla_rope_init(mla_rope *rope, double base, int interleaved, double factor, int original_len, double beta_fast,
+                  double beta_slow, double magnitude);
+
+/*
+ * Rotates the rotary dims of query rows into place beside mla_head_gemm's latent ones: row (i, h) of
+ * x (64 bf16 at x + i * ldx + h * x_head_stride) goes to y + i * ldy + h * y_head_stride, i < tokens,
+ * h < heads. For the decode's q [.., h_q, 576], y = q + 512, y_head_stride = 576. x = y (in place) is
+ * allowed; other overlaps are not.
+ *   positions   int32[tokens], any int32 value; or NULL: token i is query token i % s_q of sequence
+ *               i / s_q, at position max(seqlens[i / s_q], 0) + i % s_q (seqlens int32[tokens / s_q]: the
+ *               lengths BEFORE the new tokens, as for the appends)
+ *   rope        host pointer, read during the call
+ * Strides are in elements, non-negative multiples of 8; x and y 16-byte aligned; tokens in [1, 2^24],
+ * heads in [1, 4096]. Angles and products in fp32, one rounding to bf16 (nearest even). Asynchronous on
+ * `stream`; allocates nothing. Errors as for mla_head_gemm.
+ */
+int mla_rope_q(const void *x, int64_t ldx, int64_t x_head_stride, void *y, int64_t ldy, int64_t y_head_stride, int tokens,
+               int heads, const int32_t *positions, const int32_t *seqlens, int s_q, const mla_rope *rope,
+               void *stream);
+
+/*
+ * The cache append with the work that comes before it in the same pass: the latent's RMS norm and the
+ * rotation of the rotary dims. Token i (a row of 576 bf16 at new_kv + i * ld) is stored as
+ *     latent: x * rsqrt(mean(x^2) + eps) * norm_weight over its 512 latent dims (norm_weight NULL: x)
+ *     rotary: the 64 rotary dims turned to the token's position (see mla_rope)
+ * each rounded once to the cache's type (mla_append_kv / mla_append_kv_fp8's rules for rows, types and
+ * kv_scale).
+ *   cu_new      NULL: tokens = batch * n_new, token t of sequence b is row b * n_new + t. Otherwise int32
+ *               [batch + 1], non-decreasing: packed sequences, rows [cu_new[b], cu_new[b+1]) are those of
+ *               sequence b (none, if equal), n_new is not used, and rows outside [cu_new[0], cu_new[batch])
+ *               are not read into the cache
+ *   norm_weight bf16[512], 16-byte aligned, or NULL; eps >= 0
+ *   positions   int32[tokens], or NULL: the position within the sequence, seqlens[b] + t
+ *   ld          elements between rows, >= 576, a multiple of 8
+ *   seqlens     int32[batch]: the lengths BEFORE the append
+ * tokens in [0, 2^30] (0: a no-op). Two tokens of one call must not share a cache row. Asynchronous on
+ * `stream`; allocates nothing; a token whose table entry is missing or out of range is skipped and reported
+ * as MLA_ERR_BOUNDS by mla_check_status.
+ */
+int mla_append_kv_rope(const void *new_kv, int64_t ld, int64_t tokens, int n_new, const int32_t *cu_new,
+                       const void *norm_weight, float eps, const mla_rope *rope, const int32_t *positions,
+                       void *kv_cache, int64_t num_blocks, const int32_t *block_table, int64_t bt_stride,
+                       const int32_t *seqlens, int batch, void *stream);
+int mla_append_kv_rope_fp8(const void *new_kv, int64_t ld, int64_t tokens, int n_new, const int32_t *cu_new,
+                           const void *norm_weight, float eps, const mla_rope *rope, const int32_t *positions,
+                           void *kv_cache_fp8, int64_t num_blocks, float kv_scale, const int32_t *block_table,
+                           int64_t bt_stride, const int32_t *seqlens, int batch, void *stream);
+
+/*
  * End-to-end call on HOST buffers: copies the inputs host->device, runs metadata +
  * decode, copies out/lse device->host, and synchronises `stream` before returning.
  * Host buffers should be pinned for the copies to be asynchronous. `dev` holds the

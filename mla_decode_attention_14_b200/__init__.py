@@ -16,6 +16,7 @@ lse fp32 [b, h_q, s_q].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -41,6 +42,8 @@ STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
 EXPORTS = ("mla_status_string", "mla_default_num_parts", "mla_default_fixed_cost", "mla_workspace_bytes",
            "mla_get_metadata", "mla_decode", "mla_decode_split", "mla_decode_combine", "mla_decode_fp8",
            "mla_decode_split_fp8", "mla_get_metadata_sparse", "mla_decode_sparse", "mla_append_kv", "mla_append_kv_fp8", "mla_head_gemm",
+           "mla_shared_units", "mla_shared_fixed_cost", "mla_shared_workspace_bytes", "mla_get_metadata_shared",
+           "mla_decode_shared", "mla_rope_init", "mla_rope_q", "mla_append_kv_rope", "mla_append_kv_rope_fp8",
            "mla_decode_host", "mla_decode_host_fp8",
            "mla_decode_noalloc", "mla_check_status", "mla_launch_count", "mla_last_cuda_error",
            "mla_selftest_wait_timeout")
@@ -60,6 +63,10 @@ class _DeviceBuffers(ctypes.Structure):
                 ("seqlens", ctypes.c_void_p), ("tile_meta", ctypes.c_void_p), ("num_splits", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t), ("num_parts", ctypes.c_int), ("fixed_cost", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * 32), ("magnitude", ctypes.c_float), ("interleaved", ctypes.c_int32)]
 
 
 def lib():
@@ -109,6 +116,26 @@ def lib():
         L.mla_decode_host_fp8.argtypes = [P, P, I64, F, P, I64, P, I, I, I, F, I, P, P,
                                           ctypes.POINTER(_DeviceBuffers), P]
         L.mla_decode_host_fp8.restype = I
+        L.mla_shared_units.argtypes = [I, I, I, I]
+        L.mla_shared_units.restype = I64
+        L.mla_shared_fixed_cost.argtypes = []
+        L.mla_shared_fixed_cost.restype = I
+        L.mla_shared_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.mla_shared_workspace_bytes.restype = SZ
+        L.mla_get_metadata_shared.argtypes = [P, I, I, I, I, I, I, P, P, P]
+        L.mla_get_metadata_shared.restype = I
+        L.mla_decode_shared.argtypes = [P, P, I64, P, I, P, I64, P, P, P, I, I, I, I, F, I, P, P, P, SZ, P]
+        L.mla_decode_shared.restype = I
+        D, RP = ctypes.c_double, ctypes.POINTER(_Rope)
+        L.mla_rope_init.argtypes = [RP, D, I, D, I, D, D, D]
+        L.mla_rope_init.restype = I
+        L.mla_rope_q.argtypes = [P, I64, I64, P, I64, I64, I, I, P, P, I, RP, P]
+        L.mla_rope_q.restype = I
+        app = [P, I64, I64, I, P, P, F, RP, P, P, I64, P, I64, P, I, P]
+        L.mla_append_kv_rope.argtypes = app
+        L.mla_append_kv_rope.restype = I
+        L.mla_append_kv_rope_fp8.argtypes = app[:11] + [F] + app[11:]  # kv_scale after num_blocks
+        L.mla_append_kv_rope_fp8.restype = I
         L.mla_check_status.argtypes = [P]
         L.mla_check_status.restype = I
         L.mla_launch_count.argtypes = []
@@ -154,6 +181,12 @@ class Metadata:
     h_q: int
     s_q: int
     topk: int = 0             # sparse mode (get_metadata_sparse): keys per query token; 0 = dense
+
+
+@dataclass
+class SharedMetadata(Metadata):
+    """Schedule of :func:`decode_shared`, produced by :func:`get_metadata_shared`."""
+    shared_blocks: int = 0
 
 
 def default_num_parts(h_q: int, s_q: int, device=None) -> int:
@@ -253,6 +286,8 @@ def _decode_args(q, kv_cache, block_table, seqlens, meta):
     b, s_q, h_q, d = q.shape
     if d != D_QK:
         raise ValueError("q last dim must be %d" % D_QK)
+    if isinstance(meta, SharedMetadata):
+        raise ValueError("metadata was computed for decode_shared (use get_metadata)")
     if kv_cache is not None:  # bf16 cache (the fp8 one is checked by decode_fp8)
         _need(kv_cache, "kv_cache", torch.bfloat16)
         if kv_cache.dim() == 4:
@@ -364,6 +399,268 @@ def absorb_o(o_latent: torch.Tensor, w_uv: torch.Tensor, out: torch.Tensor | Non
     if out is None:
         out = torch.empty((b, s_q, h, d), dtype=torch.bfloat16, device=o_latent.device)
     return head_gemm(o_latent, h * D_V, D_V, w_uv, out, h * d, d, b * s_q, d, D_V, h, stream)
+
+
+def _on(dev: torch.device):
+    """Makes ``dev`` the current device for a call (nothing to do when it is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _stream_on(dev: torch.device, stream) -> int:
+    """The stream a call on ``dev`` goes to: the caller's, else that device's current one."""
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _same_device(dev: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+
+
+def get_metadata_shared(seqlens: torch.Tensor, h_q: int, s_q: int, shared_blocks: int, num_parts: int | None = None,
+                        fixed_cost: int | None = None, stream=None) -> SharedMetadata:
+    """Schedule for :func:`decode_shared` (``mla_get_metadata_shared``): ``seqlens`` int32 ``[b]`` are whole
+    lengths, the ``shared_blocks`` prefix blocks of 64 tokens included."""
+    _need(seqlens, "seqlens", torch.int32, 1)
+    dev, b = seqlens.device, seqlens.shape[0]
+    if num_parts is None:
+        num_parts = default_num_parts(1, 1, dev)  # one part per pair of SMs
+    if fixed_cost is None:
+        fixed_cost = lib().mla_shared_fixed_cost()
+    units = lib().mla_shared_units(b, s_q, h_q, shared_blocks)
+    if units < 1:
+        raise MLAError("mla_shared_units", 1)
+    tm = torch.empty((num_parts, META_INTS), dtype=torch.int32, device=dev)
+    ns = torch.empty((units + 1,), dtype=torch.int32, device=dev)
+    with _on(dev):
+        _check("mla_get_metadata_shared", lib().mla_get_metadata_shared(
+            seqlens.data_ptr(), b, s_q, h_q, shared_blocks, num_parts, fixed_cost, tm.data_ptr(), ns.data_ptr(),
+            _stream_on(dev, stream)))
+    return SharedMetadata(tm, ns, num_parts, fixed_cost, h_q, s_q, 0, shared_blocks)
+
+
+def shared_workspace_bytes(batch: int, s_q: int, h_q: int, shared_blocks: int, num_parts: int) -> int:
+    return lib().mla_shared_workspace_bytes(batch, s_q, h_q, shared_blocks, num_parts)
+
+
+def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, shared_table: torch.Tensor, block_table: torch.Tensor,
+                  seqlens: torch.Tensor, scale: float, causal: bool, meta: SharedMetadata,
+                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """MLA decode for a batch that shares a cached prefix (``mla_decode_shared``).
+
+    ``shared_table`` int32 ``[shared_blocks]``: the prefix's blocks; row b of ``block_table`` holds sequence b's
+    blocks from entry ``shared_blocks`` on (earlier entries are not read); ``seqlens`` are whole lengths.
+    Returns ``(out bf16 [b, s_q, h_q, 512], lse fp32 [b, h_q, s_q])``, as :func:`decode` with tables that
+    all begin with ``shared_table``.
+    """
+    _need(q, "q", torch.bfloat16, 4)
+    _need(kv_cache, "kv_cache", torch.bfloat16)
+    _need(shared_table, "shared_table", torch.int32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seqlens, "seqlens", torch.int32, 1)
+    b, s_q, h_q, d = q.shape
+    shared_blocks, dev = shared_table.shape[0], q.device
+    if d != D_QK or kv_cache.dim() not in (3, 4) or kv_cache.shape[1] != BLOCK or kv_cache.shape[-1] != D_QK or \
+            kv_cache.numel() != kv_cache.shape[0] * BLOCK * D_QK:
+        raise ValueError("q must be [b, s_q, h_q, 576] and kv_cache [num_blocks, 64, 1, 576]")
+    if block_table.shape[0] != b or seqlens.shape[0] != b:
+        raise ValueError("batch mismatch between q, block_table and seqlens")
+    if not isinstance(meta, SharedMetadata) or (meta.h_q, meta.s_q, meta.shared_blocks) != (h_q, s_q, shared_blocks) or \
+            meta.num_splits.shape[0] != lib().mla_shared_units(b, s_q, h_q, shared_blocks) + 1:
+        raise ValueError("metadata was computed for another shape (use get_metadata_shared)")
+    if out is None:
+        out = torch.empty((b, s_q, h_q, D_V), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, 4)
+        if out.shape != (b, s_q, h_q, D_V):
+            raise ValueError("out must be [b, s_q, h_q, 512]")
+    if lse is None:
+        lse = torch.empty((b, h_q, s_q), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32, 3)
+        if lse.shape != (b, h_q, s_q):
+            raise ValueError("lse must be [b, h_q, s_q]")
+    ws_bytes = lib().mla_shared_workspace_bytes(b, s_q, h_q, shared_blocks, meta.num_parts)
+    if workspace is None:
+        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < ws_bytes:
+        raise ValueError("workspace must be a contiguous CUDA tensor of at least %d bytes" % ws_bytes)
+    _same_device(dev, kv_cache=kv_cache, shared_table=shared_table, block_table=block_table, seqlens=seqlens, out=out,
+                 lse=lse, workspace=workspace, meta=meta.tile_meta)
+    with _on(dev):
+        _check("mla_decode_shared", lib().mla_decode_shared(
+            q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], shared_table.data_ptr(), shared_blocks,
+            block_table.data_ptr(), block_table.shape[1], seqlens.data_ptr(), meta.tile_meta.data_ptr(),
+            meta.num_splits.data_ptr(), meta.num_parts, b, s_q, h_q, scale, 1 if causal else 0, out.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), ws_bytes, _stream_on(dev, stream)))
+    return out, lse
+
+
+class Rope:
+    """Rotary frequencies, magnitude and layout for :func:`rope_q` and the rotating appends (a host-side
+    ``mla_rope``; made by :func:`rope`)."""
+
+    def __init__(self, c: _Rope):
+        self.c = c
+        self.ref = ctypes.byref(c)
+
+    @property
+    def interleaved(self) -> bool:
+        return bool(self.c.interleaved)
+
+    @property
+    def magnitude(self) -> float:
+        return self.c.magnitude
+
+    @property
+    def turns(self) -> list:
+        """Full turns per position of each of the 32 pairs, times 2^64."""
+        return list(self.c.turns)
+
+
+def rope(base: float = 10000.0, interleaved: bool = True, factor: float = 1.0, original_len: int = 0,
+         beta_fast: float = 32.0, beta_slow: float = 1.0, magnitude: float = 1.0) -> Rope:
+    """Rotary positions of the 64 rotary dims (``mla_rope_init``): frequencies ``base ** (-2i / 64)``, for
+    ``factor`` > 1 interpolated (piecewise over ``original_len`` positions, or all of them when that is 0)."""
+    c = _Rope()
+    _check("mla_rope_init", lib().mla_rope_init(ctypes.byref(c), base, 1 if interleaved else 0, factor, original_len,
+                                                beta_fast, beta_slow, magnitude))
+    return Rope(c)
+
+
+def _row_strides(t: torch.Tensor, name: str, tokens_dims: int):
+    """(stride between tokens, between heads) of t[tokens..., heads, dims], in elements; 0 for a single one."""
+    if t.stride(-1) != 1:
+        raise ValueError("%s must have its last dim contiguous" % name)
+    sizes, strides = t.shape, t.stride()
+    if tokens_dims == 1:
+        ld = strides[0] if sizes[0] > 1 else 0
+    elif sizes[1] == 1:
+        ld = strides[0] if sizes[0] > 1 else 0
+    else:
+        ld = strides[1]
+        if sizes[0] > 1 and strides[0] != sizes[1] * ld:
+            raise ValueError("%s must have evenly spaced tokens" % name)
+    return ld, strides[-2] if sizes[-2] > 1 else 0
+
+
+def rope_q(x: torch.Tensor, q: torch.Tensor, rope: Rope, seqlens: torch.Tensor | None = None,
+           positions: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotates query rows' rotary dims: ``q[..., 512:] = rotate(x)`` (``mla_rope_q``); returns ``q``.
+
+    ``x`` bf16 ``[b, s_q, h, 64]`` or packed ``[tokens, h, 64]``, a view with any 16-byte aligned strides (for
+    example the last dims of the up-projected queries, or ``q[..., 512:]`` itself); ``q`` bf16 of the same shape
+    with 576 dims. ``positions`` int32, one per token; without it (4-D only) token t of sequence b is at
+    ``seqlens[b] + t``, seqlens int32 ``[b]`` being the lengths before the new tokens.
+    """
+    nd = x.dim()
+    if x.dtype != torch.bfloat16 or q.dtype != torch.bfloat16:
+        raise TypeError("x and q must be bfloat16, got %s and %s" % (x.dtype, q.dtype))
+    if not x.is_cuda or not q.is_cuda:
+        raise ValueError("x and q must be CUDA tensors")
+    if nd not in (3, 4) or x.shape[-1] != D_QK - D_V or q.shape != x.shape[:-1] + (D_QK,):
+        raise ValueError("shapes: x [b, s_q, h, 64] and q [b, s_q, h, 576], or x [tokens, h, 64] and q [tokens, h, 576]")
+    dev = x.device
+    tokens, s_q = x.shape[0], 1
+    if nd == 4:
+        s_q = x.shape[1]
+        tokens *= s_q
+    if positions is not None:
+        _need(positions, "positions", torch.int32)
+        if positions.numel() != tokens:
+            raise ValueError("positions must hold one value per token")
+    elif nd == 3 or seqlens is None:
+        raise ValueError("positions must be given for packed tokens; seqlens or positions otherwise")
+    else:
+        _need(seqlens, "seqlens", torch.int32, 1)
+        if seqlens.shape[0] != x.shape[0]:
+            raise ValueError("batch mismatch between x and seqlens")
+    _same_device(dev, q=q, seqlens=seqlens, positions=positions)
+    if x.numel() == 0:
+        return q
+    ldx, hx = _row_strides(x, "x", nd - 2)
+    ldq, hq = _row_strides(q, "q", nd - 2)
+    with _on(dev):
+        _check("mla_rope_q", lib().mla_rope_q(
+            x.data_ptr(), ldx, hx, q.data_ptr() + 2 * D_V, ldq, hq, tokens, x.shape[-2],
+            None if positions is None else positions.data_ptr(),
+            None if positions is not None else seqlens.data_ptr(), s_q, rope.ref, _stream_on(dev, stream)))
+    return q
+
+
+def _append_rope(fp8, new_kv, kv_cache, block_table, seqlens, kv_scale, rope, norm_weight, eps, positions, cu_new, stream):
+    fn = "mla_append_kv_rope_fp8" if fp8 else "mla_append_kv_rope"
+    if new_kv.dtype != torch.bfloat16:
+        raise TypeError("new_kv must be bfloat16, got %s" % new_kv.dtype)
+    if not new_kv.is_cuda:
+        raise ValueError("new_kv must be a CUDA tensor")
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seqlens, "seqlens", torch.int32, 1)
+    _need(kv_cache, "kv_cache", torch.uint8 if fp8 else torch.bfloat16)
+    dev, b, width = new_kv.device, seqlens.shape[0], FP8_RECORD_BYTES if fp8 else D_QK
+    if new_kv.shape[-1] != D_QK or new_kv.dim() != (3 if cu_new is None else 2):
+        raise ValueError("new_kv must be [b, n_new, 576], or [tokens, 576] with cu_new")
+    if kv_cache.dim() not in (3, 4) or kv_cache.shape[1] != BLOCK or kv_cache.shape[-1] != width or \
+            kv_cache.numel() != kv_cache.shape[0] * BLOCK * width:
+        raise ValueError("the cache must be [num_blocks, 64, 1, %d]" % width)
+    if block_table.shape[0] != b:
+        raise ValueError("batch mismatch between block_table and seqlens")
+    if cu_new is None:
+        if new_kv.shape[0] != b:
+            raise ValueError("batch mismatch between new_kv and seqlens")
+        n_new = new_kv.shape[1]
+        tokens = b * n_new
+    else:
+        _need(cu_new, "cu_new", torch.int32, 1)
+        if cu_new.shape[0] != b + 1:
+            raise ValueError("cu_new must hold b + 1 values")
+        tokens, n_new = new_kv.shape[0], 0
+    if norm_weight is not None:
+        _need(norm_weight, "norm_weight", torch.bfloat16, 1)
+        if norm_weight.shape[0] != D_V:
+            raise ValueError("norm_weight must hold 512 values")
+    if positions is not None:
+        _need(positions, "positions", torch.int32)
+        if positions.numel() != tokens:
+            raise ValueError("positions must hold one value per token")
+    _same_device(dev, cache=kv_cache, block_table=block_table, seqlens=seqlens, cu_new=cu_new, norm_weight=norm_weight,
+                 positions=positions)
+    if tokens == 0:
+        return
+    # a row stands where a head does in _row_strides' layout: one of them per token
+    ld = _row_strides(new_kv.unsqueeze(-2), "new_kv", new_kv.dim() - 1)[0] or D_QK
+    scale = (kv_scale,) if fp8 else ()
+    with _on(dev):
+        _check(fn, getattr(lib(), fn)(
+            new_kv.data_ptr(), ld, tokens, n_new, None if cu_new is None else cu_new.data_ptr(),
+            None if norm_weight is None else norm_weight.data_ptr(), eps, rope.ref,
+            None if positions is None else positions.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], *scale,
+            block_table.data_ptr(), block_table.shape[1], seqlens.data_ptr(), b, _stream_on(dev, stream)))
+
+
+def append_kv_rope(new_kv: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor,
+                   rope: Rope, norm_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                   positions: torch.Tensor | None = None, cu_new: torch.Tensor | None = None, stream=None) -> None:
+    """:func:`append_kv` with the latent's RMS norm (``norm_weight`` bf16 ``[512]``, or None) and the rotation
+    of the rotary dims on the way (``mla_append_kv_rope``).
+
+    ``new_kv`` bf16 ``[b, n_new, 576]``, or packed ``[tokens, 576]`` with ``cu_new`` int32 ``[b + 1]`` (rows
+    ``cu_new[b]`` to ``cu_new[b + 1]`` belong to sequence b); rows may be strided (a wider projection's).
+    ``seqlens`` are the lengths before the append; ``positions`` int32, one per token, default to the
+    position within the sequence.
+    """
+    _append_rope(False, new_kv, kv_cache, block_table, seqlens, None, rope, norm_weight, eps, positions, cu_new, stream)
+
+
+def append_kv_rope_fp8(new_kv: torch.Tensor, kv_cache_fp8: torch.Tensor, block_table: torch.Tensor,
+                       seqlens: torch.Tensor, kv_scale: float, rope: Rope, norm_weight: torch.Tensor | None = None,
+                       eps: float = 1e-6, positions: torch.Tensor | None = None, cu_new: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """The same into the fp8 cache (``mla_append_kv_rope_fp8``): the (normed) latent as E4M3 codes of
+    ``x * (1 / kv_scale)``, the rotary dims as bf16."""
+    _append_rope(True, new_kv, kv_cache_fp8, block_table, seqlens, kv_scale, rope, norm_weight, eps, positions, cu_new,
+                 stream)
 
 
 def decode_fp8(q: torch.Tensor, kv_cache_fp8: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor,

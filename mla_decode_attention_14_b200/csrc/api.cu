@@ -10,6 +10,8 @@
 
 #include "../../include/mla.h"
 #include "common.cuh"
+#include "rope.cuh"
+#include "shared.cuh"
 
 namespace mla {
 
@@ -25,6 +27,15 @@ cudaError_t launch_head_gemm(const CUtensorMap &map_x, const CUtensorMap &map_w,
 cudaError_t launch_append(const __nv_bfloat16 *new_kv, int n_new, void *kv, int64_t num_blocks,
                           const int32_t *block_table, int64_t bt_stride, const int32_t *seqlens, int batch,
                           bool fp8, float inv_scale, cudaStream_t stream);
+
+cudaError_t launch_shared_metadata(const int32_t *seqlens, int batch, int groups, int prefix_units, int shared_blocks,
+                                   int num_parts, int fixed_cost, int32_t *tile_meta, int32_t *num_splits,
+                                   cudaStream_t stream);
+cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                          const CUtensorMap &map_q, cudaStream_t stream);
+cudaError_t launch_shared_merge(const SharedParams &p, cudaStream_t stream);
+cudaError_t launch_rope_query(const rp::QueryParams &p, const mla_rope &rope, cudaStream_t stream);
+cudaError_t launch_append_rope(const rp::AppendParams &p, const mla_rope &rope, bool fp8, cudaStream_t stream);
 
 static std::atomic<int64_t> g_launches{0};
 static std::atomic<int> g_last_cuda_error{0};  // cudaError_t of the last failing CUDA call
@@ -150,6 +161,31 @@ int sparse_shape_ok(int batch, int s_q, int h_q, int topk) {
 }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Shared-prefix decode: the work units of a call (see shared.cu).
+struct SharedShape {
+    int rows, groups, own_rows;
+    int64_t total_rows, prefix_units, units;
+};
+bool shared_shape(int batch, int s_q, int h_q, int shared_blocks, SharedShape *sh) {
+    if (!shape_ok(batch, s_q, h_q) || shared_blocks < 0 || shared_blocks > (1 << 24)) return false;
+    sh->rows = s_q * h_q;
+    sh->groups = (sh->rows + 127) / 128;
+    sh->own_rows = sh->rows < 128 ? sh->rows : 128;
+    sh->total_rows = (int64_t)batch * sh->rows;
+    // 128-row tiles across sequences pay only where a sequence does not fill its own
+    sh->prefix_units = shared_blocks > 0 && sh->rows % 128 != 0 ? (sh->total_rows + 127) / 128 : 0;
+    sh->units = sh->prefix_units + (int64_t)batch * sh->groups;
+    return true;
+}
+// Partial rows: (prefix_units + num_parts) slots of 128 (where there are prefix units), then
+// (own units + num_parts) of own_rows.
+int64_t shared_own_base(const SharedShape &sh, int num_parts) {
+    return sh.prefix_units > 0 ? (sh.prefix_units + num_parts) * 128 : 0;
+}
+int64_t shared_part_rows(const SharedShape &sh, int num_parts) {
+    return shared_own_base(sh, num_parts) + (sh.units - sh.prefix_units + num_parts) * sh.own_rows;
+}
 
 // Workspace layout: fp32 o_part[(batch + num_parts) * rows * 512], then fp32
 // lse_part[(batch + num_parts) * rows], then fp32 lost_part[(batch + num_parts) * rows * 2].
@@ -498,6 +534,226 @@ int mla_head_gemm(const void *x, int64_t ldx, int64_t x_head_stride, const void 
                                      m, n, k, heads, static_cast<cudaStream_t>(stream));
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(e);
+}
+
+int64_t mla_shared_units(int batch, int s_q, int h_q, int shared_blocks) {
+    SharedShape sh;
+    return shared_shape(batch, s_q, h_q, shared_blocks, &sh) ? sh.units : 0;
+}
+
+// Per-piece start-up cost in 128-token tiles.
+int mla_shared_fixed_cost(void) { return 2; }
+
+size_t mla_shared_workspace_bytes(int batch, int s_q, int h_q, int shared_blocks, int num_parts) {
+    SharedShape sh;
+    if (!shared_shape(batch, s_q, h_q, shared_blocks, &sh) || num_parts < 1 || num_parts > 65535) return 0;
+    return round_up((size_t)shared_part_rows(sh, num_parts) * (MLA_D_V + 1) * sizeof(float), 256);
+}
+
+int mla_get_metadata_shared(const int32_t *seqlens, int batch, int s_q, int h_q, int shared_blocks, int num_parts,
+                            int fixed_cost, int32_t *tile_meta, int32_t *num_splits, void *stream) {
+    SharedShape sh;
+    if (!seqlens || !tile_meta || !num_splits) return MLA_ERR_INVALID_ARG;
+    if (!shared_shape(batch, s_q, h_q, shared_blocks, &sh) || num_parts < 1 || num_parts > 65535 || fixed_cost < 0 ||
+        fixed_cost > (1 << 20))
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned(seqlens, 4) || !aligned(tile_meta, 4) || !aligned(num_splits, 4)) return MLA_ERR_INVALID_ARG;
+    int rc = check_device();
+    if (rc != MLA_OK) return rc;
+    cudaError_t e = launch_shared_metadata(seqlens, batch, sh.groups, (int)sh.prefix_units, shared_blocks, num_parts,
+                                           fixed_cost, tile_meta, num_splits, static_cast<cudaStream_t>(stream));
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(e);
+}
+
+// A [rows, 576] bf16 tensor as [9][rows][64] with 64-row boxes of `boxes` x 64 columns (128-byte swizzle).
+static bool box_map(EncodeTiledFn enc, CUtensorMap *map, const void *base, int64_t rows, int boxes) {
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, MLA_D_QK / 64}, strides[2] = {MLA_D_QK * 2, 128};
+    cuuint32_t box[3] = {64, 64, (cuuint32_t)boxes}, estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int mla_decode_shared(const void *q, const void *kv_cache, int64_t num_blocks, const int32_t *shared_table,
+                      int shared_blocks, const int32_t *block_table, int64_t bt_stride, const int32_t *seqlens,
+                      const int32_t *tile_meta, const int32_t *num_splits, int num_parts, int batch, int s_q, int h_q,
+                      float scale, int causal, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+    SharedShape sh;
+    if (!q || !kv_cache || !block_table || !seqlens || !tile_meta || !num_splits || !out || !lse || !workspace)
+        return MLA_ERR_INVALID_ARG;
+    if (!shared_shape(batch, s_q, h_q, shared_blocks, &sh) || num_parts < 1 || num_parts > 65535)
+        return MLA_ERR_INVALID_ARG;
+    if (shared_blocks > 0 && (!shared_table || !aligned(shared_table, 4))) return MLA_ERR_INVALID_ARG;
+    if (num_blocks < 1 || num_blocks > (int64_t)(INT32_MAX / MLA_BLOCK_TOKENS)) return MLA_ERR_INVALID_ARG;
+    if (bt_stride < 1 || bt_stride > (int64_t)INT32_MAX) return MLA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale >= 0.f) || (causal != 0 && causal != 1)) return MLA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256) ||
+        !aligned(block_table, 4) || !aligned(seqlens, 4) || !aligned(tile_meta, 4) || !aligned(num_splits, 4))
+        return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < mla_shared_workspace_bytes(batch, s_q, h_q, shared_blocks, num_parts)) return MLA_ERR_WORKSPACE;
+    int rc = check_device();
+    if (rc != MLA_OK) return rc;
+    EncodeTiledFn enc = encode_fn();
+    CUtensorMap map_k, map_v, map_q;
+    if (!enc || !box_map(enc, &map_k, kv_cache, num_blocks * MLA_BLOCK_TOKENS, 9) ||
+        !box_map(enc, &map_v, kv_cache, num_blocks * MLA_BLOCK_TOKENS, 4) || !box_map(enc, &map_q, q, sh.total_rows, 9))
+        return MLA_ERR_CUDA;
+    SharedParams p;
+    p.shared_table = shared_table;
+    p.block_table = block_table;
+    p.seqlens = seqlens;
+    p.tile_meta = tile_meta;
+    p.num_splits = num_splits;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse = lse;
+    p.o_part = static_cast<float *>(workspace);
+    p.lse_part = p.o_part + (size_t)shared_part_rows(sh, num_parts) * MLA_D_V;
+    p.num_blocks = num_blocks;
+    p.bt_stride = bt_stride;
+    p.own_base = shared_own_base(sh, num_parts);
+    p.batch = batch;
+    p.s_q = s_q;
+    p.h_q = h_q;
+    p.rows = sh.rows;
+    p.total_rows = (int)sh.total_rows;
+    p.groups = sh.groups;
+    p.own_rows = sh.own_rows;
+    p.prefix_units = (int)sh.prefix_units;
+    p.units = (int)sh.units;
+    p.shared_blocks = shared_blocks;
+    p.num_parts = num_parts;
+    p.causal = causal;
+    p.out_v8 = aligned(out, 32);
+    // a masked score is -inf, and -inf * 0 is no number: scale 0 (uniform weights) becomes a scale that no
+    // finite score can tell from it
+    p.scale_log2 = std::fmax(scale * 1.4426950408889634f, 1e-37f);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_shared(p, map_k, map_v, map_q, st);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    if (e != cudaSuccess) return cuda_status(e);
+    e = launch_shared_merge(p, st);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(e);
+}
+
+int mla_rope_init(mla_rope *rope, double base, int interleaved, double factor, int original_len, double beta_fast,
+                  double beta_slow, double magnitude) {
+    if (!rope || !(base > 1.0) || !std::isfinite(base) || (interleaved != 0 && interleaved != 1) || !(factor >= 1.0) ||
+        !std::isfinite(factor) || original_len < 0 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+        !std::isfinite(beta_fast) || !std::isfinite(magnitude))
+        return MLA_ERR_INVALID_ARG;
+    constexpr int dim = MLA_D_QK - MLA_D_V;
+    const double pi = 3.14159265358979323846;
+    double low = 0.0, high = 0.0;
+    if (original_len > 0) {  // the pairs that make beta_fast and beta_slow turns over original_len positions
+        const double ln = 2.0 * std::log(base);
+        low = std::floor(dim * std::log(original_len / (beta_fast * 2.0 * pi)) / ln);
+        high = std::ceil(dim * std::log(original_len / (beta_slow * 2.0 * pi)) / ln);
+        low = std::fmin(std::fmax(low, 0.0), dim - 1.0);
+        high = std::fmin(std::fmax(high, 0.0), dim - 1.0);
+        if (high <= low) high = low + 0.001;
+    }
+    for (int i = 0; i < dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / dim);
+        // share of the interpolated frequency: 0 for fast pairs, 1 for slow ones; without original_len 1
+        const double ramp = original_len > 0 ? std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0) : 1.0;
+        const double turns = (f * (1.0 - ramp) + f / factor * ramp) / (2.0 * pi);  // per position, below 1 / 6
+        rope->turns[i] = (uint64_t)(std::ldexp(turns, 64) + 0.5);
+    }
+    rope->magnitude = (float)magnitude;
+    rope->interleaved = interleaved;
+    return MLA_OK;
+}
+
+int mla_rope_q(const void *x, int64_t ldx, int64_t x_head_stride, void *y, int64_t ldy, int64_t y_head_stride, int tokens,
+               int heads, const int32_t *positions, const int32_t *seqlens, int s_q, const mla_rope *rope,
+               void *stream) {
+    if (!x || !y || !rope || (!positions && !seqlens)) return MLA_ERR_INVALID_ARG;
+    if (tokens < 1 || tokens > (1 << 24) || heads < 1 || heads > 4096) return MLA_ERR_INVALID_ARG;
+    if (!positions && (s_q < 1 || tokens % s_q != 0)) return MLA_ERR_INVALID_ARG;
+    constexpr int64_t kMaxStride = (int64_t)1 << 40;  // element offsets stay in 64 bits
+    if (ldx % 8 || x_head_stride % 8 || ldy % 8 || y_head_stride % 8 || ldx < 0 || ldy < 0 || x_head_stride < 0 ||
+        y_head_stride < 0 || ldx > kMaxStride || ldy > kMaxStride || x_head_stride > kMaxStride ||
+        y_head_stride > kMaxStride)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(positions, 4) || !aligned(seqlens, 4)) return MLA_ERR_INVALID_ARG;
+    int rc = check_device();
+    if (rc != MLA_OK) return rc;
+    rp::QueryParams p;
+    p.x = static_cast<const __nv_bfloat16 *>(x);
+    p.y = static_cast<__nv_bfloat16 *>(y);
+    p.ldx = ldx;
+    p.x_head = x_head_stride;
+    p.ldy = ldy;
+    p.y_head = y_head_stride;
+    p.positions = positions;
+    p.seqlens = seqlens;
+    p.tokens = tokens;
+    p.heads = heads;
+    p.s_q = positions ? 1 : s_q;
+    p.chunks = 0;
+    cudaError_t e = launch_rope_query(p, *rope, static_cast<cudaStream_t>(stream));
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(e);
+}
+
+static int append_rope_common(const void *new_kv, int64_t ld, int64_t tokens, int n_new, const int32_t *cu_new,
+                              const void *norm_weight, float eps, const mla_rope *rope, const int32_t *positions,
+                              void *kv, int64_t num_blocks, const int32_t *block_table, int64_t bt_stride,
+                              const int32_t *seqlens, int batch, bool fp8, float inv_scale, void *stream) {
+    if (!new_kv || !kv || !block_table || !seqlens || !rope) return MLA_ERR_INVALID_ARG;
+    if (batch < 1 || batch > MLA_MAX_BATCH || tokens < 0 || tokens > (1 << 30)) return MLA_ERR_INVALID_ARG;
+    if (!cu_new && (n_new < 0 || (int64_t)batch * n_new != tokens)) return MLA_ERR_INVALID_ARG;
+    if (ld < MLA_D_QK || ld % 8 || ld > ((int64_t)1 << 32)) return MLA_ERR_INVALID_ARG;
+    if (num_blocks < 1 || num_blocks > (int64_t)(INT32_MAX / MLA_BLOCK_TOKENS)) return MLA_ERR_INVALID_ARG;
+    if (bt_stride < 1 || bt_stride > (int64_t)INT32_MAX) return MLA_ERR_INVALID_ARG;
+    if (norm_weight && (!std::isfinite(eps) || !(eps >= 0.f))) return MLA_ERR_INVALID_ARG;
+    if (!aligned(new_kv, 16) || !aligned(kv, 16) || !aligned(norm_weight, 16) || !aligned(block_table, 4) ||
+        !aligned(seqlens, 4) || !aligned(cu_new, 4) || !aligned(positions, 4))
+        return MLA_ERR_INVALID_ARG;
+    int rc = check_device();
+    if (rc != MLA_OK) return rc;
+    if (tokens == 0) return MLA_OK;
+    rp::AppendParams p;
+    p.x = static_cast<const __nv_bfloat16 *>(new_kv);
+    p.ld = ld;
+    p.tokens = tokens;
+    p.n_new = n_new;
+    p.cu_new = cu_new;
+    p.weight = static_cast<const __nv_bfloat16 *>(norm_weight);
+    p.eps = eps;
+    p.inv_scale = inv_scale;
+    p.positions = positions;
+    p.kv = static_cast<uint8_t *>(kv);
+    p.num_blocks = num_blocks;
+    p.bt_stride = bt_stride;
+    p.block_table = block_table;
+    p.seqlens = seqlens;
+    p.batch = batch;
+    cudaError_t e = launch_append_rope(p, *rope, fp8, static_cast<cudaStream_t>(stream));
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(e);
+}
+
+int mla_append_kv_rope(const void *new_kv, int64_t ld, int64_t tokens, int n_new, const int32_t *cu_new,
+                       const void *norm_weight, float eps, const mla_rope *rope, const int32_t *positions,
+                       void *kv_cache, int64_t num_blocks, const int32_t *block_table, int64_t bt_stride,
+                       const int32_t *seqlens, int batch, void *stream) {
+    return append_rope_common(new_kv, ld, tokens, n_new, cu_new, norm_weight, eps, rope, positions, kv_cache, num_blocks,
+                              block_table, bt_stride, seqlens, batch, false, 0.f, stream);
+}
+
+int mla_append_kv_rope_fp8(const void *new_kv, int64_t ld, int64_t tokens, int n_new, const int32_t *cu_new,
+                           const void *norm_weight, float eps, const mla_rope *rope, const int32_t *positions,
+                           void *kv_cache_fp8, int64_t num_blocks, float kv_scale, const int32_t *block_table,
+                           int64_t bt_stride, const int32_t *seqlens, int batch, void *stream) {
+    if (!std::isfinite(kv_scale) || !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+    const float inv = 1.f / kv_scale;
+    if (!std::isfinite(inv)) return MLA_ERR_INVALID_ARG;
+    return append_rope_common(new_kv, ld, tokens, n_new, cu_new, norm_weight, eps, rope, positions, kv_cache_fp8,
+                              num_blocks, block_table, bt_stride, seqlens, batch, true, inv, stream);
 }
 
 static int decode_host_common(const void *q_host, const void *kv_cache_host, int64_t num_blocks, bool fp8,

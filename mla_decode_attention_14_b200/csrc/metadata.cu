@@ -18,6 +18,7 @@
 // sequence writes the begin/end fields of the parts its blocks touch (every field is
 // written by exactly one thread).
 #include "common.cuh"
+#include "shared.cuh"
 
 namespace mla {
 
@@ -51,9 +52,11 @@ __device__ __forceinline__ T block_exclusive_scan(T v, T *warp_sums, T *total) {
     return warp_prefix + x - v;
 }
 
-__global__ void __launch_bounds__(kMetaThreads)
-metadata_kernel(const int32_t *__restrict__ seqlens, int uniform_n, int batch, int num_parts, int C,
-                int32_t *__restrict__ tile_meta, int32_t *__restrict__ num_splits) {
+// The partition of `batch` sequences, sequence i of width(i) work units (blocks), over the parts of one
+// CTA's call. `note` goes to field 5 of every part.
+template <class Width>
+__device__ __forceinline__ void partition(const Width &width, int batch, int num_parts, int C, int note,
+                                          int32_t *__restrict__ tile_meta, int32_t *__restrict__ num_splits) {
     __shared__ int64_t warp_sums64[32];
     __shared__ int32_t warp_sums32[32];
     __shared__ int64_t red[32];
@@ -61,13 +64,13 @@ metadata_kernel(const int32_t *__restrict__ seqlens, int uniform_n, int batch, i
     // empty parts first
     for (int p = threadIdx.x; p < num_parts; p += blockDim.x) {
         int32_t *m = tile_meta + (size_t)p * kMetaInts;
-        m[0] = 0; m[1] = 0; m[2] = -1; m[3] = 0; m[4] = 0; m[5] = 0; m[6] = 0; m[7] = 0;
+        m[0] = 0; m[1] = 0; m[2] = -1; m[3] = 0; m[4] = 0; m[5] = note; m[6] = 0; m[7] = 0;
     }
 
     // pass 1: total units U
     int64_t local = 0;
     for (int i = threadIdx.x; i < batch; i += blockDim.x) {
-        int w = num_blocks_of(seqlens ? seqlens[i] : uniform_n);
+        int w = width(i);
         if (w > 0) local += (int64_t)C + w;
     }
 #pragma unroll
@@ -86,7 +89,7 @@ metadata_kernel(const int32_t *__restrict__ seqlens, int uniform_n, int batch, i
     int32_t carry_splits = 0;
     for (int base = 0; base < batch; base += blockDim.x) {
         const int i = base + threadIdx.x;
-        const int w = i < batch ? num_blocks_of(seqlens ? seqlens[i] : uniform_n) : 0;
+        const int w = i < batch ? width(i) : 0;
         const int64_t cost = w > 0 ? (int64_t)C + w : 0;
         int64_t chunk_units;
         const int64_t pre = carry_units + block_exclusive_scan<int64_t>(cost, warp_sums64, &chunk_units);
@@ -119,10 +122,52 @@ metadata_kernel(const int32_t *__restrict__ seqlens, int uniform_n, int batch, i
     }
 }
 
+__global__ void __launch_bounds__(kMetaThreads)
+metadata_kernel(const int32_t *__restrict__ seqlens, int uniform_n, int batch, int num_parts, int C,
+                int32_t *__restrict__ tile_meta, int32_t *__restrict__ num_splits) {
+    partition([=](int i) { return num_blocks_of(seqlens ? seqlens[i] : uniform_n); }, batch, num_parts, C, 0, tile_meta,
+              num_splits);
+}
+
+// Shared-prefix decode: the units are prefix_units row tiles over the shared blocks, then `groups` row
+// tiles of each sequence over its own blocks (over all of its blocks when there are no prefix units), in
+// tiles of two blocks. Field 5 of a part: the prefix tokens that some sequence reaches (contents past
+// that are undefined).
+__global__ void __launch_bounds__(kMetaThreads)
+shared_metadata_kernel(const int32_t *__restrict__ seqlens, int batch, int groups, int prefix_units, int shared_blocks,
+                       int num_parts, int C, int32_t *__restrict__ tile_meta, int32_t *__restrict__ num_splits) {
+    __shared__ int warp_max[kMetaThreads / 32];
+    int top = 0;
+    for (int i = threadIdx.x; i < batch; i += blockDim.x) top = max(top, seqlens[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int k = 0; k < kMetaThreads / 32; ++k) top = max(top, warp_max[k]);
+    const int prefix_tok = min(top, shared_blocks * kBlk);
+    const int skip = prefix_units > 0 ? shared_blocks : 0;
+    partition(
+        [=](int u) {
+            const int blocks = u < prefix_units
+                                   ? num_blocks_of(prefix_tok)
+                                   : num_blocks_of(clamp_len(seqlens[(u - prefix_units) / groups])) - skip;
+            return (max(blocks, 0) + 1) / 2;
+        },
+        prefix_units + batch * groups, num_parts, C, prefix_tok, tile_meta, num_splits);
+}
+
 cudaError_t launch_metadata(const int32_t *seqlens, int uniform_n, int batch, int num_parts, int fixed_cost,
                             int32_t *tile_meta, int32_t *num_splits, cudaStream_t stream) {
     metadata_kernel<<<1, kMetaThreads, 0, stream>>>(seqlens, uniform_n, batch, num_parts, fixed_cost,
                                                     tile_meta, num_splits);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_shared_metadata(const int32_t *seqlens, int batch, int groups, int prefix_units, int shared_blocks,
+                                   int num_parts, int fixed_cost, int32_t *tile_meta, int32_t *num_splits,
+                                   cudaStream_t stream) {
+    shared_metadata_kernel<<<1, kMetaThreads, 0, stream>>>(seqlens, batch, groups, prefix_units, shared_blocks, num_parts,
+                                                           fixed_cost, tile_meta, num_splits);
     return cudaGetLastError();
 }
 

@@ -8,3 +8,5 @@
 #include "selftest.cu"
 #include "append.cu"
 #include "head_gemm.cu"
+#include "shared.cu"
+#include "rope.cu"

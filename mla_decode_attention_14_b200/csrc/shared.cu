@@ -1,0 +1,664 @@
+// shared.cu -- MLA decode attention for a batch whose sequences begin with the same cached prefix.
+//
+// The result is that of mla_decode: per query row r of sequence b, over the V visible keys of b,
+//   s_j = scale <q_r, k_j>,  lse = log sum_j e^{s_j},  out = sum_j e^{s_j - lse} k_j[0:512].
+// The sum over keys splits at the end of the prefix, and each part's normalised result and lse merge
+// exactly (up to rounding): lse = log(e^{lse_1} + e^{lse_2}), out = sum_i e^{lse_i - lse} out_i. The
+// prefix keys are the same for every row of the batch, so its part is ONE attention of all batch * s_q *
+// h_q rows over one key list: the rows fill 128-row tensor tiles whatever the head count (16 heads alone
+// fill an eighth of one) and a key block is read once per tile of rows, not once per sequence.
+//
+// Work units (partitioned into parts by metadata.cu, in 128-token tiles):
+//  * rows per sequence not a multiple of 128: first ceil(rows of the batch / 128) prefix units (128
+//    rows of the flat [batch * s_q * h_q] row space, the shared blocks), then one unit per (sequence,
+//    128-row group) over the sequence's own blocks;
+//  * a multiple of 128 (every row tile belongs to one sequence) or no shared block: one unit per
+//    (sequence, group) over shared and own blocks alike, so that an unsplit unit needs no merge.
+// A unit cut into pieces, or one of the first kind, leaves fp32 partials for the combine kernel.
+//
+// The kernel: one persistent 2-CTA pair per part, MMAs with cta_group::2.
+//  * 128 rows x 512 value dims of fp32 output are a whole SM's tensor memory, so a pair shares a tile:
+//    64 rows in each CTA. M = 128 over the pair puts a CTA's 64 rows into all of its 128 TMEM lanes
+//    (lane l: row l % 64; lanes 64-127 hold the upper half of the columns): O takes 256 columns and the
+//    scores of 128 tokens 64, so two score buffers fit beside it and no partial score or probability
+//    ever crosses between the SMs.
+//  * A tile is two cache blocks; CTA h loads block h whole (73,728 bytes, one TMA operation; K-major
+//    boxes of 64 tokens x 64 dims): its half of Gemm1's B operand. S = Q K^T: 36 MMAs of 128 x 128 x 16.
+//  * O += P V: 16 MMAs of 128 x 256 x 16 (MN-major B). CTA h provides value dims [256h, 256h + 256) of
+//    all 128 tokens: of its own block in place, of the other block loaded once more (32,768 bytes, from L2)
+//    over boxes that Gemm1 has finished with -- boxes 4-7 of CTA 0, 0-3 of CTA 1, so that the two
+//    CTAs' operands sit at the same offsets, as one descriptor needs. P (bf16) of block 0 goes over the
+//    dead rotary box, of block 1 into 8 KB of its own: two 128-token stages and Q fit in 227 KB.
+//  * Eight softmax warps, one thread per (row, 32 tokens); the four threads of a row agree on the running
+//    maximum through shared memory, O is rescaled only when it grows by more than 2^8 (P <= 2^8, exact
+//    in the fp32 sums). P is rounded to bf16 once (to nearest): an error of at most 2^-9 of each term,
+//    the size of the output's own rounding, where a second term would add half to the MMA time.
+//  * Roles: warp 0 = K and Q loads; warp 2 = the other block's value half, zeroing of rows past the
+//    unit's end (undefined contents must not meet a zero probability); warps 1 and 3 of the leader
+//    issue Gemm1 and Gemm2; warps 4-11 softmax and epilogue.
+// Every wait is bounded; a timeout sets the device error word and the pair exits cleanly.
+#include "pair_ptx.cuh"
+#include "shared.cuh"
+
+namespace mla {
+using namespace sm100;
+
+namespace shr {
+constexpr int kTileTok = kSharedTileTok;       // 128 tokens: one cache block per CTA
+constexpr int kSoftWarps = 8, kThreads = 32 * (4 + kSoftWarps);
+constexpr int kStages = 2;
+constexpr int kBox = kBlk * 128;               // 64 rows x 64 bf16, 128-byte swizzle
+constexpr int kBoxes = kDqk / 64;              // 9
+constexpr int kStageBytes = kBoxes * kBox;     // 73,728: one cache block, or 64 query rows
+constexpr int kOtherBytes = 4 * kBox;          // the other block's 256 value dims
+constexpr float kRescaleThreshold = 8.0f;      // log2 units
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemSCols = 64, kTmemCols = 512;
+
+struct __align__(1024) Smem {
+    uint8_t q[kStageBytes];
+    uint8_t stage[kStages][kStageBytes];
+    uint8_t p1[kBox];                          // P of the tile's second block (the first's: the rotary box)
+    float xmax[2][4][64];                      // block maxima of a row's four threads; their sums at the end
+    // leader's: k_full, q_full (TMA of both CTAs), v_ready, p_ready (arrivals of both); both CTAs': the rest
+    uint64_t k_full[kStages], q_full, v_full[kStages], v_ready[kStages], p_ready[kStages];
+    uint64_t s_full[kStages], pv_done[kStages], mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Smem) <= 232448, "shared memory must fit 227 KB");
+
+// One piece: tiles [lo, hi) of a unit. Tile t holds blocks first_blk + 2t and the next, up to end_blk.
+struct Piece {
+    int seq, group;  // seq < 0: a prefix unit
+    int lo, hi, first_blk, end_blk, end_tok, nsplit;
+    int64_t part_row;  // first row of its partial slot
+};
+
+struct Walker {
+    int unit, begin_unit, begin_tile, end_unit, end_tile, first_piece, prefix_tok;
+    Piece pc;
+    int tile, piece_k;
+    bool live;
+
+    __device__ bool next_piece(const SharedParams &p) {
+        while (unit <= end_unit) {
+            const int u = unit++;
+            if (u < p.prefix_units) {
+                pc.seq = -1;
+                pc.group = u;
+                pc.first_blk = 0;
+                pc.end_tok = prefix_tok;
+            } else {
+                const int o = u - p.prefix_units;
+                pc.seq = o / p.groups;
+                pc.group = o % p.groups;
+                pc.first_blk = p.prefix_units > 0 ? p.shared_blocks : 0;
+                pc.end_tok = clamp_len(__ldg(&p.seqlens[pc.seq]));
+            }
+            pc.end_blk = num_blocks_of(pc.end_tok);
+            const int w = (max(pc.end_blk - pc.first_blk, 0) + 1) / 2;
+            pc.lo = u == begin_unit ? max(begin_tile, 0) : 0;
+            pc.hi = u == end_unit ? min(end_tile, w) : w;
+            if (pc.hi <= pc.lo) continue;
+            // partial slots: the prefix units' of 128 rows, then the own units' of own_rows
+            const int s0 = __ldg(&p.num_splits[u]), own0 = __ldg(&p.num_splits[p.prefix_units]);
+            pc.nsplit = __ldg(&p.num_splits[u + 1]) - s0;
+            const int slot = s0 + (u == begin_unit ? first_piece : 0) - (pc.seq < 0 ? 0 : own0);
+            const int slots = (pc.seq < 0 ? p.prefix_units : p.units - p.prefix_units) + p.num_parts;
+            if (pc.nsplit < 1 || slot < 0 || slot >= slots) continue;  // malformed
+            pc.part_row = pc.seq < 0 ? (int64_t)slot * 128 : p.own_base + (int64_t)slot * p.own_rows;
+            return true;
+        }
+        return false;
+    }
+    __device__ void init(const int32_t *meta, const SharedParams &p) {
+        begin_unit = meta[0];
+        begin_tile = meta[1];
+        end_unit = meta[2];
+        end_tile = meta[3];
+        first_piece = meta[4];
+        prefix_tok = min(max(meta[5], 0), p.shared_blocks * kBlk);
+        if (end_unit >= begin_unit && (begin_unit < 0 || end_unit >= p.units)) end_unit = begin_unit - 1;  // malformed
+        unit = begin_unit;
+        piece_k = -1;
+        step(p);
+    }
+    __device__ void step(const SharedParams &p) {
+        live = next_piece(p);
+        tile = live ? pc.lo : 0;
+        ++piece_k;
+    }
+    __device__ bool first() const { return tile == pc.lo; }
+    __device__ bool last() const { return tile == pc.hi - 1; }
+    __device__ int blk() const { return pc.first_blk + 2 * tile; }
+    __device__ void advance(const SharedParams &p) {
+        if (++tile >= pc.hi) step(p);
+    }
+    // flat row of q that starts this CTA's 64 rows
+    __device__ int q_row(const SharedParams &p, int rank) const {
+        return (pc.seq < 0 ? 0 : pc.seq * p.rows) + pc.group * 128 + rank * 64;
+    }
+};
+
+// Cache row of block `blk` of the piece, or one past the cache (TMA then fills zeros) when the piece has
+// no such block or its table entry is out of range.
+__device__ __forceinline__ int block_row(const SharedParams &p, const Piece &pc, int blk, bool &bad) {
+    const int none = (int)(p.num_blocks * kBlk);
+    if (blk >= pc.end_blk) return none;
+    int phys;
+    if (blk < p.shared_blocks)
+        phys = __ldg(&p.shared_table[blk]);
+    else
+        phys = blk < p.bt_stride ? __ldg(&p.block_table[(size_t)pc.seq * p.bt_stride + blk]) : -1;
+    if (phys < 0 || (int64_t)phys >= p.num_blocks) {
+        bad = true;
+        return none;
+    }
+    return phys * kBlk;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int lane) {
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait(bar, parity, abort);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+// the same for a barrier that threads of the other CTA arrive on
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, int lane) {
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait_cluster(bar, parity, abort);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// ---------------------------------------------------------------- warp 0, one thread: K tiles and Q
+__device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_k, const CUtensorMap *map_q,
+                          const int32_t *meta, uint32_t rank) {
+    const uint64_t pol_shared = l2_evict_normal_policy(), pol_own = l2_evict_first_policy();
+    Walker w;
+    w.init(meta, p);
+    bool bad = false;
+    int g = 0, pieces = 0;
+    for (; w.live; w.advance(p), ++g) {
+        const int s = g % kStages;
+        if (g >= kStages && !mbar_wait(&sm.pv_done[s], (g / kStages - 1) & 1, &sm.abort)) break;
+        const int blk = w.blk() + (int)rank;
+        const int y = block_row(p, w.pc, blk, bad);
+        if (rank == 0) mbar_arrive_expect_tx(&sm.k_full[s], 2 * kStageBytes);
+        tma_load_3d_pair(sm.stage[s], map_k, 0, y, 0, map_to_rank(&sm.k_full[s], 0),
+                         blk < p.shared_blocks ? pol_shared : pol_own);
+        if (w.first()) {  // Q follows once Gemm1 of the previous piece's last tile has read the old one
+            if (g > 0 && !mbar_wait(&sm.s_full[(g - 1) % kStages], ((g - 1) / kStages) & 1, &sm.abort)) {
+                ++g;
+                break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kStageBytes);
+            tma_load_3d_pair(sm.q, map_q, 0, w.q_row(p, (int)rank), 0, map_to_rank(&sm.q_full, 0), pol_own);
+            ++pieces;
+        }
+    }
+    if (bad) raise_error(kErrBounds);
+    // loads still in flight must land before the pair exits (the leader's barriers see both CTAs' loads)
+    if (rank == 0) {
+        for (int k = max(0, g - kStages); k < g; ++k) {
+            const long long t0 = clock64();
+            while (!mbar_sleep_test(&sm.k_full[k % kStages], (k / kStages) & 1) && clock64() - t0 < kSpinCycles) {
+            }
+        }
+        if (pieces > 0) {
+            const long long t0 = clock64();
+            while (!mbar_sleep_test(&sm.q_full, (pieces - 1) & 1) && clock64() - t0 < kSpinCycles) {
+            }
+        }
+    }
+}
+
+// Zero this CTA's value rows past the unit's end in block t of the tile (t's 4 boxes at 4t).
+__device__ void zero_rows(uint8_t *boxes, int valid, int lane) {
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    for (int e = lane; e < (kBlk - valid) * 8; e += 32) {
+        const int off = (valid + (e >> 3)) * 128 + ((e & 7) << 4);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) *reinterpret_cast<uint4 *>(boxes + b * kBox + off) = z;
+    }
+}
+
+// ---------------------------------------------------------------- warp 2: the other block's value half
+__device__ void value_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_v, const int32_t *meta,
+                           uint32_t rank) {
+    const uint64_t policy = l2_evict_normal_policy();
+    const int lane = threadIdx.x & 31;
+    Walker w;
+    w.init(meta, p);
+    bool bad = false;
+    for (int g = 0; w.live; w.advance(p), ++g) {
+        const int s = g % kStages;
+        const uint32_t ph = (g / kStages) & 1;
+        const int other = 1 - (int)rank;
+        if (!warp_wait(&sm.s_full[s], ph, &sm.abort, lane)) break;  // Gemm1 is done with the boxes
+        if (lane == 0) {
+            const int y = block_row(p, w.pc, w.blk() + other, bad);
+            mbar_arrive_expect_tx(&sm.v_full[s], kOtherBytes);
+            tma_load_3d(sm.stage[s] + 4 * other * kBox, map_v, 0, y, 4 * (int)rank, &sm.v_full[s], policy);
+        }
+        __syncwarp();
+        if (!warp_wait(&sm.v_full[s], ph, &sm.abort, lane)) break;
+        // valid tokens of the tile's blocks (a missing block was filled with zeros)
+        const int left = w.pc.end_tok - w.blk() * kBlk;
+        if (left < kTileTok) {
+            if (left < kBlk) zero_rows(sm.stage[s], max(left, 0), lane);
+            if (left > kBlk) zero_rows(sm.stage[s] + 4 * kBox, left - kBlk, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_remote(&sm.v_ready[s], 0);
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- warps 1 and 3 of the leader: MMAs
+__device__ void gemm1_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem) {
+    constexpr uint32_t id = idesc_bf16_f32(128, 128, 0);
+    const int lane = threadIdx.x & 31;
+    const uint64_t qd = smem_desc(smem_addr(sm.q), 16, 1024, 2);
+    Walker w;
+    w.init(meta, p);
+    for (int g = 0; w.live; w.advance(p), ++g) {
+        const int s = g % kStages;
+        if (!warp_wait_cluster(&sm.k_full[s], (g / kStages) & 1, &sm.abort, lane)) break;
+        if (w.first() && !warp_wait_cluster(&sm.q_full, w.piece_k & 1, &sm.abort, lane)) break;
+        // the score buffer is free: K of this tile was loaded after Gemm2 of tile g - 2, which needed its P
+        tc_fence_after();
+        const uint64_t kd = smem_desc(smem_addr(sm.stage[s]), 16, 1024, 2);
+        const uint32_t d = tmem + kTmemS + kTmemSCols * s;
+        if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kDqk / 16; ++k) {
+                const uint64_t off = (uint64_t)(((k >> 2) * kBox + (k & 3) * 32) >> 4);
+                mma_ss_pair(d, qd + off, kd + off, id, k > 0 ? 1u : 0u);
+            }
+            mma_commit_pair(&sm.s_full[s]);
+        }
+        __syncwarp();
+    }
+}
+
+__device__ void gemm2_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem) {
+    constexpr uint32_t id = idesc_bf16_f32(128, 256, 1);  // MN-major B
+    const int lane = threadIdx.x & 31;
+    const uint64_t p1d = smem_desc(smem_addr(sm.p1), 16, 1024, 2);
+    Walker w;
+    w.init(meta, p);
+    for (int g = 0; w.live; w.advance(p), ++g) {
+        const int s = g % kStages;
+        const uint32_t ph = (g / kStages) & 1;
+        if (!warp_wait_cluster(&sm.v_ready[s], ph, &sm.abort, lane)) break;
+        if (!warp_wait_cluster(&sm.p_ready[s], ph, &sm.abort, lane)) break;
+        tc_fence_after();
+        const uint64_t p0d = smem_desc(smem_addr(sm.stage[s] + 8 * kBox), 16, 1024, 2);
+        const uint64_t vd = smem_desc(smem_addr(sm.stage[s]), kBox, 1024, 2);
+        const uint32_t acc0 = w.first() ? 0u : 1u;
+        if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {  // 16 tokens each; block t = k / 4
+                const uint64_t a = (k < 4 ? p0d : p1d) + 2 * (k & 3);
+                const uint64_t b = vd + (uint64_t)(((k >> 2) * 4 * kBox + (k & 3) * 2048) >> 4);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)  // 128 value dims of each CTA
+                    mma_ss_pair(tmem + kTmemO + 128 * n, a, b + (uint64_t)((2 * n * kBox) >> 4), id,
+                                k > 0 ? 1u : acc0);
+            }
+            mma_commit_pair(&sm.pv_done[s]);
+        }
+        __syncwarp();
+    }
+}
+
+// Every MMA this warp issued completes before teardown (bounded; independent of the abort flag).
+__device__ void drain_mmas(Smem &sm) {
+    if (elect_one()) {
+        mma_commit_pair_local(&sm.mma_done);
+        const long long t0 = clock64();
+        while (!mbar_sleep_test(&sm.mma_done, 0) && clock64() - t0 < kSpinCycles) {
+        }
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- warps 4-11: softmax and epilogue
+// Warp w: TMEM lane quarter w & 3 (rows 32 (w & 1) .. + 32 of the CTA's 64; block (w >> 1) & 1 of the tile),
+// 32 of that block's tokens (th). Of O, its lanes hold dims [256 blk + 128 th, + 128) of its rows.
+__device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem, uint32_t rank) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wq = warp & 3, blk = wq >> 1, th = (warp - 4) >> 2;
+    const int i = (wq & 1) * 32 + lane;  // row of this CTA's 64
+    const int bar_id = 1 + (wq & 1);     // the four warps of these 32 rows
+    const int x = 2 * blk + th;          // this thread's place among the row's four
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const float sl2 = p.scale_log2;
+    // After a failed wait the warp walks on without waiting, so that no named barrier misses it.
+    bool dead = false;
+    const auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, &sm.abort)) dead = true;
+        __syncwarp();
+    };
+    Walker w;
+    w.init(meta, p);
+    float m_ref = -INFINITY, l = 0.f;
+    int vis = 0, flat = 0;
+    bool row_ok = false;
+    for (int g = 0; w.live; ++g) {
+        const int s = g % kStages;
+        const uint32_t ph = (g / kStages) & 1;
+        const bool first = w.first();
+        if (first) {  // this row's visible keys within the piece
+            flat = w.q_row(p, (int)rank) + i;
+            const int seq = w.pc.seq < 0 ? min(flat, p.total_rows - 1) / p.rows : w.pc.seq;
+            const int r = flat - seq * p.rows;
+            row_ok = w.pc.seq < 0 ? flat < p.total_rows : r < p.rows;
+            vis = row_ok ? visible_keys(__ldg(&p.seqlens[seq]), p.s_q, r / p.h_q, p.causal) : 0;
+            vis = min(vis, min(w.pc.first_blk + 2 * w.pc.hi, w.pc.end_blk) * kBlk);
+        }
+        const int key0 = w.blk() * kBlk + blk * kBlk + 32 * th;
+        wait(&sm.s_full[s], ph);
+        tc_fence_after();
+        uint32_t raw[32];
+        tmem_ld32(tmem + kTmemS + kTmemSCols * s + lane_off + 32 * th, raw);
+        tmem_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+        if (key0 + 32 > vis) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = key0 + j < vis ? v[j] : -INFINITY;
+        }
+        sm.xmax[g & 1][x][i] = max32(v);
+        named_bar_sync(bar_id, 128);
+        const float mx = fmaxf(fmaxf(sm.xmax[g & 1][0][i], sm.xmax[g & 1][1][i]),
+                               fmaxf(sm.xmax[g & 1][2][i], sm.xmax[g & 1][3][i]));
+        const float mb = mx == -INFINITY ? -INFINITY : mx * sl2;  // sl2 > 0: the maximum commutes with it
+        bool need = false;
+        float alpha = 1.f;
+        if (first) {
+            m_ref = mb;
+            l = 0.f;
+        } else if (mb > m_ref + kRescaleThreshold) {
+            if (m_ref != -INFINITY) {  // else nothing is accumulated yet: O and l are zero
+                alpha = ex2_approx(m_ref - mb);
+                l *= alpha;
+                need = true;
+            }
+            m_ref = mb;
+        }
+        const float off = m_ref == -INFINITY ? 0.f : -m_ref;
+        const f32x2 sc = pack2(sl2, sl2), of = pack2(off, off);
+        f32x2 su[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            float a, b;
+            unpack2(fma2(pack2(v[j], v[j + 1]), sc, of), a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            su[(j >> 1) & 3] = add2(su[(j >> 1) & 3], pack2(a, b));
+            __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
+            pk[j >> 1] = *reinterpret_cast<uint32_t *>(&two);
+        }
+        {
+            float a, b;
+            unpack2(add2(add2(su[0], su[1]), add2(su[2], su[3])), a, b);
+            l += a + b;
+        }
+        // Gemm2 of the previous tile is done with P's second box and with O
+        if (g > 0) wait(&sm.pv_done[(g - 1) % kStages], ((g - 1) / kStages) & 1);
+        if (__any_sync(0xffffffffu, need)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tmem + kTmemO + lane_off + 128 * th + 16 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st16(tmem + kTmemO + lane_off + 128 * th + 16 * c, o);
+            }
+            tmem_wait_st();
+        }
+        uint8_t *prow = (blk == 0 ? sm.stage[s] + 8 * kBox : sm.p1) + i * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(prow + (((4 * th + c) ^ (i & 7)) << 4)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(&sm.p_ready[s], 0);
+
+        if (w.last()) {
+            // the row's four sums, through the maxima's slots of the other parity (read before the barrier above)
+            sm.xmax[(g + 1) & 1][x][i] = l;
+            named_bar_sync(bar_id, 128);
+            const float lr = (sm.xmax[(g + 1) & 1][0][i] + sm.xmax[(g + 1) & 1][1][i]) +
+                             (sm.xmax[(g + 1) & 1][2][i] + sm.xmax[(g + 1) & 1][3][i]);
+            named_bar_sync(bar_id, 128);  // read before the next tile's maxima take the slots
+            const bool empty = lr == 0.f;
+            const float inv = empty ? 0.f : 1.f / lr;
+            const float lse2 = empty ? -INFINITY : m_ref + log2f(lr);
+            const bool whole = p.prefix_units == 0 && w.pc.nsplit == 1;
+            const int64_t part_row = w.pc.part_row + (int)rank * 64 + i;
+            wait(&sm.pv_done[s], ph);
+            tc_fence_after();
+            const int col = 256 * blk + 128 * th;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tmem + kTmemO + lane_off + 128 * th + 16 * c, o);
+                tmem_wait_ld();
+                if (!row_ok) continue;
+                if (whole) {
+                    uint32_t wv[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv,
+                                                                   __uint_as_float(o[2 * j + 1]) * inv);
+                        wv[j] = *reinterpret_cast<uint32_t *>(&two);
+                    }
+                    __nv_bfloat16 *dst = p.out + (size_t)flat * kDv + col + 16 * c;
+                    if (p.out_v8) {
+                        st_global_v8(dst, wv);
+                    } else {
+                        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+                        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+                    }
+                } else {
+                    float *dst = p.o_part + (size_t)part_row * kDv + col + 16 * c;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+                    st_global_v8(dst, o);
+                    st_global_v8(dst + 8, o + 8);
+                }
+            }
+            if (row_ok && x == 0) {
+                if (whole) {
+                    const int r = flat % p.rows;
+                    p.lse[((size_t)(flat / p.rows) * p.h_q + r % p.h_q) * p.s_q + r / p.h_q] =
+                        lse2 * 0.69314718055994530942f;
+                } else {
+                    p.lse_part[part_row] = lse2;
+                }
+            }
+            tc_fence_before();  // ordered before the next tile's P, which lets Gemm2 overwrite O
+        }
+        w.advance(p);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+              const __grid_constant__ CUtensorMap map_q, const SharedParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of it is used: no room to align by hand
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    const uint32_t rank = cluster_ctarank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t *meta = p.tile_meta + (size_t)(blockIdx.x >> 1) * kMetaInts;
+    if (smem_addr(smem_raw) & 1023) {  // the swizzled boxes need it; both CTAs of the pair see the same
+        if (threadIdx.x == 0) raise_error(kErrBounds);
+        return;
+    }
+
+    if (warp == 1) tmem_alloc_pair(&sm.tmem_base, kTmemCols);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.k_full[s], 1);
+            mbar_init(&sm.v_full[s], 1);
+            mbar_init(&sm.v_ready[s], 2);
+            mbar_init(&sm.p_ready[s], 2 * kSoftWarps);
+            mbar_init(&sm.s_full[s], 1);
+            mbar_init(&sm.pv_done[s], 1);
+        }
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.mma_done, 2);
+        sm.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        prefetch_tensormap(&map_q);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) load_role(sm, p, &map_k, &map_q, meta, rank);
+    } else if (warp == 2) {
+        value_role(sm, p, &map_v, meta, rank);
+    } else if (warp == 1) {
+        if (rank == 0) {
+            gemm1_role(sm, p, meta, tmem);
+            drain_mmas(sm);
+        }
+    } else if (warp == 3) {
+        if (rank == 0) {
+            gemm2_role(sm, p, meta, tmem);
+            drain_mmas(sm);
+        }
+    } else {
+        softmax_role(sm, p, meta, tmem, rank);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && sm.abort) raise_error(kErrTimeout);
+    cluster_sync();  // nothing of the pair is in flight any more
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- merging the pieces of a row
+// One warp per row: the pieces of its prefix unit, then those of its own unit; 16 dims per lane.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const SharedParams p) {
+    const int flat = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (flat >= p.total_rows) return;
+    const int seq = flat / p.rows, r = flat % p.rows;
+    const int pu = flat / 128, ou = p.prefix_units + seq * p.groups + r / 128;
+    const int o0 = p.num_splits[ou], no = p.num_splits[ou + 1] - o0;
+    const int p0 = p.prefix_units > 0 ? p.num_splits[pu] : 0, np = p.prefix_units > 0 ? p.num_splits[pu + 1] - p0 : 0;
+    const int ob = p.num_splits[p.prefix_units];
+    if (p.prefix_units == 0 && no == 1) return;  // written by the attention kernel
+    if (no < 0 || np < 0 || o0 < 0 || p0 < 0 || no + np > 2 * p.num_parts + 2 ||
+        o0 + no > p.units + p.num_parts || p0 + np > p.units + p.num_parts || o0 < ob) {  // malformed metadata
+        if (lane == 0) raise_error(kErrBounds);
+        return;
+    }
+    const int64_t prow = (int64_t)p0 * 128 + flat % 128;
+    const int64_t orow = p.own_base + (int64_t)(o0 - ob) * p.own_rows + r % 128;
+    const int ns = np + no;
+    const auto row_of = [&](int k) { return k < np ? prow + (int64_t)k * 128 : orow + (int64_t)(k - np) * p.own_rows; };
+    float m = -INFINITY;
+    for (int k = lane; k < ns; k += 32) m = fmaxf(m, p.lse_part[row_of(k)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+    float sum = 0.f;
+    if (m != -INFINITY) {
+        for (int k0 = 0; k0 < ns; k0 += 4) {  // four pieces' loads in flight
+            float w[4];
+            float4 v[4][4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const bool on = k0 + d < ns;
+                const int64_t row = row_of(on ? k0 + d : 0);
+                w[d] = on ? exp2f(p.lse_part[row] - m) : 0.f;
+                const float4 *src = reinterpret_cast<const float4 *>(p.o_part + (size_t)row * kDv + 16 * lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[d][j] = on ? src[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                if (w[d] == 0.f) continue;  // no key in the piece, or a negligible weight
+                sum += w[d];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[4 * j + 0] = fmaf(w[d], v[d][j].x, acc[4 * j + 0]);
+                    acc[4 * j + 1] = fmaf(w[d], v[d][j].y, acc[4 * j + 1]);
+                    acc[4 * j + 2] = fmaf(w[d], v[d][j].z, acc[4 * j + 2]);
+                    acc[4 * j + 3] = fmaf(w[d], v[d][j].w, acc[4 * j + 3]);
+                }
+            }
+        }
+        const float inv = 1.f / sum;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[j] *= inv;
+    }
+    uint4 packed[2];
+    uint32_t *pw = reinterpret_cast<uint32_t *>(packed);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        __nv_bfloat162 two = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
+        pw[k] = *reinterpret_cast<uint32_t *>(&two);
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)flat * kDv + 16 * lane);
+    dst[0] = packed[0];
+    dst[1] = packed[1];
+    if (lane == 0)
+        p.lse[((size_t)seq * p.h_q + r % p.h_q) * p.s_q + r / p.h_q] =
+            m == -INFINITY ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
+}
+}  // namespace shr
+
+size_t shared_smem_bytes() { return sizeof(shr::Smem); }
+
+cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                          const CUtensorMap &map_q, cudaStream_t stream) {
+    const size_t smem = shared_smem_bytes();
+    cudaError_t e = cudaFuncSetAttribute(shr::shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * p.num_parts, 1, 1);
+    cfg.blockDim = dim3(shr::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, shr::shared_kernel, map_k, map_v, map_q, p);
+}
+
+cudaError_t launch_shared_merge(const SharedParams &p, cudaStream_t stream) {
+    const unsigned grid = (unsigned)((p.total_rows + shr::kMergeWarps - 1) / shr::kMergeWarps);
+    shr::merge_kernel<<<grid, 32 * shr::kMergeWarps, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace mla
