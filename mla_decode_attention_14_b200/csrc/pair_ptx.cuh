@@ -18,6 +18,45 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// Bounded waits that poll instead of sleeping: a thread suspended on a barrier wakes up to about a
+// thousand cycles after the phase completes, which the short dependent steps of a pair kernel cannot
+// hide. One lane polls for its warp. Same contract as mbar_wait (false: *abort was set, or the bound
+// passed and *abort is now set).
+__device__ __forceinline__ bool mbar_poll_once(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (mbar_poll_once(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int k = 0; k < 64; ++k)
+            if (mbar_poll_once(bar, parity)) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > kSpinCycles) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool warp_poll(uint64_t *bar, uint32_t parity, volatile int *abort, int lane) {
+    bool ok = true;
+    if (lane == 0) ok = mbar_poll(bar, parity, abort);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// Arrive on a barrier of either CTA given by its shared::cluster address, in order with this thread's own
+// accesses. What it announces lies in this CTA's shared memory, written through fence.proxy.async, and is
+// read there by the tensor core, so no fence over the cluster goes with it (a release at cluster scope
+// measured about 2,000 cycles here, with loads in flight).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // True in one lane of a converged warp. The compiler knows the region behind it to be warp-uniform and
 // keeps descriptors in uniform registers; behind `lane == 0` it moves each operand of each MMA there
 // (measured: 77 cycles an MMA instead of the tensor core's own 32 for 128 x 128 x 16).

@@ -59,9 +59,14 @@ struct __align__(1024) Smem {
     uint8_t stage[kStages][kStageBytes];
     uint8_t p1[kBox];                          // P of the tile's second block (the first's: the rotary box)
     float xmax[2][4][64];                      // block maxima of a row's four threads; their sums at the end
-    // leader's: k_full, q_full (TMA of both CTAs), v_ready, p_ready (arrivals of both); both CTAs': the rest
-    uint64_t k_full[kStages], q_full, v_full[kStages], v_ready[kStages], p_ready[kStages];
-    uint64_t s_full[kStages], pv_done[kStages], mma_done;
+    // leader's, completed by both CTAs' loads: a tile's boxes 0-3 and 8, its boxes 4-7, Q, the value halves
+    uint64_t ka_full[kStages], kb_full[kStages], q_full, v_full[kStages];
+    // a piece's last, partial tile instead: this CTA's value half; both CTAs' after zeroing (leader's)
+    uint64_t tail_full, tail_ready;
+    uint64_t p_full[kStages];     // leader's: both CTAs' softmax warps
+    // commits to both CTAs: Gemm1; Gemm2 over the tile's first block; over both
+    uint64_t s_full[kStages], pv_half[kStages], pv_done[kStages];
+    uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
 };
@@ -130,6 +135,8 @@ struct Walker {
     }
     __device__ bool first() const { return tile == pc.lo; }
     __device__ bool last() const { return tile == pc.hi - 1; }
+    // the unit ends inside the tile: rows past its end hold undefined contents
+    __device__ bool tail() const { return pc.end_tok - blk() * kBlk < kTileTok; }
     __device__ int blk() const { return pc.first_blk + 2 * tile; }
     __device__ void advance(const SharedParams &p) {
         if (++tile >= pc.hi) step(p);
@@ -157,39 +164,40 @@ __device__ __forceinline__ int block_row(const SharedParams &p, const Piece &pc,
     return phys * kBlk;
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int lane) {
-    bool ok = true;
-    if (lane == 0) ok = mbar_wait(bar, parity, abort);
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-}
-// the same for a barrier that threads of the other CTA arrive on
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, int lane) {
-    bool ok = true;
-    if (lane == 0) ok = mbar_wait_cluster(bar, parity, abort);
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+// Before the pair exits: the loads of a barrier's fill have landed (bounded; independent of the abort flag).
+__device__ void landed(uint64_t *bar, int fill) {
+    const long long t0 = clock64();
+    while (!mbar_sleep_test(bar, fill & 1) && clock64() - t0 < kSpinCycles) {
+    }
 }
 
 // ---------------------------------------------------------------- warp 0, one thread: K tiles and Q
-__device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_k, const CUtensorMap *map_q,
-                          const int32_t *meta, uint32_t rank) {
+__device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_v, const CUtensorMap *map_r,
+                          const CUtensorMap *map_q, const int32_t *meta, uint32_t rank) {
     const uint64_t pol_shared = l2_evict_normal_policy(), pol_own = l2_evict_first_policy();
     Walker w;
     w.init(meta, p);
     bool bad = false;
-    int g = 0, pieces = 0;
-    for (; w.live; w.advance(p), ++g) {
+    int g = 0, g_b = 0, pieces = 0;  // loads issued: first parts of tiles, second parts, queries
+    for (; w.live; w.advance(p)) {
         const int s = g % kStages;
-        if (g >= kStages && !mbar_wait(&sm.pv_done[s], (g / kStages - 1) & 1, &sm.abort)) break;
+        const uint32_t ph = (g / kStages - 1) & 1;
         const int blk = w.blk() + (int)rank;
         const int y = block_row(p, w.pc, blk, bad);
-        if (rank == 0) mbar_arrive_expect_tx(&sm.k_full[s], 2 * kStageBytes);
-        tma_load_3d_pair(sm.stage[s], map_k, 0, y, 0, map_to_rank(&sm.k_full[s], 0),
-                         blk < p.shared_blocks ? pol_shared : pol_own);
+        const uint64_t pol = blk < p.shared_blocks ? pol_shared : pol_own;
+        // boxes 0-3 and 8 are free once Gemm2 has taken the tile's first block, the others after the second
+        if (g >= kStages && !mbar_poll(&sm.pv_half[s], ph, &sm.abort)) break;
+        if (rank == 0) mbar_arrive_expect_tx(&sm.ka_full[s], 2 * 5 * kBox);
+        const uint32_t ka = map_to_rank(&sm.ka_full[s], 0), kb = map_to_rank(&sm.kb_full[s], 0);
+        tma_load_3d_pair(sm.stage[s], map_v, 0, y, 0, ka, pol);
+        tma_load_3d_pair(sm.stage[s] + 8 * kBox, map_r, 0, y, 8, ka, pol);
+        ++g;
+        if (g > kStages && !mbar_poll(&sm.pv_done[s], ph, &sm.abort)) break;
+        if (rank == 0) mbar_arrive_expect_tx(&sm.kb_full[s], 2 * kOtherBytes);
+        tma_load_3d_pair(sm.stage[s] + 4 * kBox, map_v, 0, y, 4, kb, pol);
+        ++g_b;
         if (w.first()) {  // Q follows once Gemm1 of the previous piece's last tile has read the old one
-            if (g > 0 && !mbar_wait(&sm.s_full[(g - 1) % kStages], ((g - 1) / kStages) & 1, &sm.abort)) {
-                ++g;
-                break;
-            }
+            if (g > 1 && !mbar_poll(&sm.s_full[(g - 2) % kStages], ((g - 2) / kStages) & 1, &sm.abort)) break;
             if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kStageBytes);
             tma_load_3d_pair(sm.q, map_q, 0, w.q_row(p, (int)rank), 0, map_to_rank(&sm.q_full, 0), pol_own);
             ++pieces;
@@ -198,20 +206,13 @@ __device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *ma
     if (bad) raise_error(kErrBounds);
     // loads still in flight must land before the pair exits (the leader's barriers see both CTAs' loads)
     if (rank == 0) {
-        for (int k = max(0, g - kStages); k < g; ++k) {
-            const long long t0 = clock64();
-            while (!mbar_sleep_test(&sm.k_full[k % kStages], (k / kStages) & 1) && clock64() - t0 < kSpinCycles) {
-            }
-        }
-        if (pieces > 0) {
-            const long long t0 = clock64();
-            while (!mbar_sleep_test(&sm.q_full, (pieces - 1) & 1) && clock64() - t0 < kSpinCycles) {
-            }
-        }
+        for (int k = max(0, g - kStages); k < g; ++k) landed(&sm.ka_full[k % kStages], k / kStages);
+        for (int k = max(0, g_b - kStages); k < g_b; ++k) landed(&sm.kb_full[k % kStages], k / kStages);
+        if (pieces > 0) landed(&sm.q_full, pieces - 1);
     }
 }
 
-// Zero this CTA's value rows past the unit's end in block t of the tile (t's 4 boxes at 4t).
+// Zero this CTA's value rows past the unit's end in one block of the tile (its 4 boxes).
 __device__ void zero_rows(uint8_t *boxes, int valid, int lane) {
     const uint4 z = make_uint4(0, 0, 0, 0);
     for (int e = lane; e < (kBlk - valid) * 8; e += 32) {
@@ -226,32 +227,44 @@ __device__ void value_role(Smem &sm, const SharedParams &p, const CUtensorMap *m
                            uint32_t rank) {
     const uint64_t policy = l2_evict_normal_policy();
     const int lane = threadIdx.x & 31;
+    const int other = 1 - (int)rank;
     Walker w;
     w.init(meta, p);
     bool bad = false;
-    for (int g = 0; w.live; w.advance(p), ++g) {
+    int tails = 0, g = 0;
+    for (; w.live; w.advance(p), ++g) {
         const int s = g % kStages;
-        const uint32_t ph = (g / kStages) & 1;
-        const int other = 1 - (int)rank;
-        if (!warp_wait(&sm.s_full[s], ph, &sm.abort, lane)) break;  // Gemm1 is done with the boxes
+        const bool tail = w.tail();
+        const int y = block_row(p, w.pc, w.blk() + other, bad);
+        if (!warp_poll(&sm.s_full[s], (g / kStages) & 1, &sm.abort, lane)) break;  // Gemm1 has read the boxes
+        uint8_t *dst = sm.stage[s] + 4 * other * kBox;
+        if (!tail) {
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive_expect_tx(&sm.v_full[s], 2 * kOtherBytes);
+                tma_load_3d_pair(dst, map_v, 0, y, 4 * (int)rank, map_to_rank(&sm.v_full[s], 0), policy);
+            }
+            __syncwarp();
+            continue;
+        }
         if (lane == 0) {
-            const int y = block_row(p, w.pc, w.blk() + other, bad);
-            mbar_arrive_expect_tx(&sm.v_full[s], kOtherBytes);
-            tma_load_3d(sm.stage[s] + 4 * other * kBox, map_v, 0, y, 4 * (int)rank, &sm.v_full[s], policy);
+            mbar_arrive_expect_tx(&sm.tail_full, kOtherBytes);
+            tma_load_3d(dst, map_v, 0, y, 4 * (int)rank, &sm.tail_full, policy);
+            if (rank == 0) mbar_arrive(&sm.v_full[s]);  // keeps the phases of the whole tiles' barrier in step
         }
         __syncwarp();
-        if (!warp_wait(&sm.v_full[s], ph, &sm.abort, lane)) break;
-        // valid tokens of the tile's blocks (a missing block was filled with zeros)
-        const int left = w.pc.end_tok - w.blk() * kBlk;
-        if (left < kTileTok) {
-            if (left < kBlk) zero_rows(sm.stage[s], max(left, 0), lane);
-            if (left > kBlk) zero_rows(sm.stage[s] + 4 * kBox, left - kBlk, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        if (lane == 0) mbar_arrive_remote(&sm.v_ready[s], 0);
+        if (!warp_poll(&sm.tail_full, tails & 1, &sm.abort, lane)) break;
+        ++tails;
+        const int left = w.pc.end_tok - w.blk() * kBlk;  // tokens of the tile (a missing block is zeros)
+        if (left < kBlk) zero_rows(sm.stage[s], max(left, 0), lane);
+        if (left > kBlk && left < kTileTok) zero_rows(sm.stage[s] + 4 * kBox, left - kBlk, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(map_to_rank(&sm.tail_ready, 0));
         __syncwarp();
     }
+    if (rank == 0 && lane == 0)
+        for (int k = max(0, g - kStages); k < g; ++k) landed(&sm.v_full[k % kStages], k / kStages);
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- warps 1 and 3 of the leader: MMAs
@@ -263,17 +276,29 @@ __device__ void gemm1_role(Smem &sm, const SharedParams &p, const int32_t *meta,
     w.init(meta, p);
     for (int g = 0; w.live; w.advance(p), ++g) {
         const int s = g % kStages;
-        if (!warp_wait_cluster(&sm.k_full[s], (g / kStages) & 1, &sm.abort, lane)) break;
-        if (w.first() && !warp_wait_cluster(&sm.q_full, w.piece_k & 1, &sm.abort, lane)) break;
-        // the score buffer is free: K of this tile was loaded after Gemm2 of tile g - 2, which needed its P
-        tc_fence_after();
+        const uint32_t ph = (g / kStages) & 1;
         const uint64_t kd = smem_desc(smem_addr(sm.stage[s]), 16, 1024, 2);
         const uint32_t d = tmem + kTmemS + kTmemSCols * s;
+        // the score buffer is free: K of this tile was loaded after Gemm2 of tile g - 2, which needed its P
+        if (w.first() && !warp_poll(&sm.q_full, w.piece_k & 1, &sm.abort, lane)) break;
+        if (!warp_poll(&sm.ka_full[s], ph, &sm.abort, lane)) break;
+        tc_fence_after();
+        if (elect_one()) {  // boxes 0-3 and 8, while the others land
+#pragma unroll
+            for (int k = 0; k < 20; ++k) {
+                const int box = k < 16 ? k >> 2 : 8;
+                const uint64_t off = (uint64_t)((box * kBox + (k & 3) * 32) >> 4);
+                mma_ss_pair(d, qd + off, kd + off, id, k > 0 ? 1u : 0u);
+            }
+        }
+        __syncwarp();
+        if (!warp_poll(&sm.kb_full[s], ph, &sm.abort, lane)) break;
+        tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kDqk / 16; ++k) {
+            for (int k = 16; k < 32; ++k) {
                 const uint64_t off = (uint64_t)(((k >> 2) * kBox + (k & 3) * 32) >> 4);
-                mma_ss_pair(d, qd + off, kd + off, id, k > 0 ? 1u : 0u);
+                mma_ss_pair(d, qd + off, kd + off, id, 1u);
             }
             mma_commit_pair(&sm.s_full[s]);
         }
@@ -287,11 +312,17 @@ __device__ void gemm2_role(Smem &sm, const SharedParams &p, const int32_t *meta,
     const uint64_t p1d = smem_desc(smem_addr(sm.p1), 16, 1024, 2);
     Walker w;
     w.init(meta, p);
+    int tails = 0;
     for (int g = 0; w.live; w.advance(p), ++g) {
         const int s = g % kStages;
         const uint32_t ph = (g / kStages) & 1;
-        if (!warp_wait_cluster(&sm.v_ready[s], ph, &sm.abort, lane)) break;
-        if (!warp_wait_cluster(&sm.p_ready[s], ph, &sm.abort, lane)) break;
+        if (w.tail()) {
+            if (!warp_poll(&sm.tail_ready, tails & 1, &sm.abort, lane)) break;
+            ++tails;
+        } else if (!warp_poll(&sm.v_full[s], ph, &sm.abort, lane)) {
+            break;
+        }
+        if (!warp_poll(&sm.p_full[s], ph, &sm.abort, lane)) break;
         tc_fence_after();
         const uint64_t p0d = smem_desc(smem_addr(sm.stage[s] + 8 * kBox), 16, 1024, 2);
         const uint64_t vd = smem_desc(smem_addr(sm.stage[s]), kBox, 1024, 2);
@@ -305,6 +336,7 @@ __device__ void gemm2_role(Smem &sm, const SharedParams &p, const int32_t *meta,
                 for (int n = 0; n < 2; ++n)  // 128 value dims of each CTA
                     mma_ss_pair(tmem + kTmemO + 128 * n, a, b + (uint64_t)((2 * n * kBox) >> 4), id,
                                 k > 0 ? 1u : acc0);
+                if (k == 3) mma_commit_pair(&sm.pv_half[s]);
             }
             mma_commit_pair(&sm.pv_done[s]);
         }
@@ -334,11 +366,11 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
     const int x = 2 * blk + th;          // this thread's place among the row's four
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const float sl2 = p.scale_log2;
+    const uint32_t p_full0 = map_to_rank(&sm.p_full[0], 0), p_full1 = map_to_rank(&sm.p_full[1], 0);
     // After a failed wait the warp walks on without waiting, so that no named barrier misses it.
     bool dead = false;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity, &sm.abort)) dead = true;
-        __syncwarp();
+        if (!dead && !warp_poll(bar, parity, &sm.abort, lane)) dead = true;
     };
     Walker w;
     w.init(meta, p);
@@ -430,7 +462,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(&sm.p_ready[s], 0);
+        if (lane == 0) mbar_arrive_pair(s == 0 ? p_full0 : p_full1);
 
         if (w.last()) {
             // the row's four sums, through the maxima's slots of the other parity (read before the barrier above)
@@ -492,7 +524,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+shared_kernel(const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_r,
               const __grid_constant__ CUtensorMap map_q, const SharedParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of it is used: no room to align by hand
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -507,19 +539,22 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     if (warp == 1) tmem_alloc_pair(&sm.tmem_base, kTmemCols);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.k_full[s], 1);
+            mbar_init(&sm.ka_full[s], 1);
+            mbar_init(&sm.kb_full[s], 1);
             mbar_init(&sm.v_full[s], 1);
-            mbar_init(&sm.v_ready[s], 2);
-            mbar_init(&sm.p_ready[s], 2 * kSoftWarps);
+            mbar_init(&sm.p_full[s], 2 * kSoftWarps);
             mbar_init(&sm.s_full[s], 1);
+            mbar_init(&sm.pv_half[s], 1);
             mbar_init(&sm.pv_done[s], 1);
         }
         mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.tail_full, 1);
+        mbar_init(&sm.tail_ready, 2);
         mbar_init(&sm.mma_done, 2);
         sm.abort = 0;
         fence_mbar_init();
-        prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
+        prefetch_tensormap(&map_r);
         prefetch_tensormap(&map_q);
     }
     tc_fence_before();
@@ -529,7 +564,7 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const uint32_t tmem = sm.tmem_base;
 
     if (warp == 0) {
-        if (lane == 0) load_role(sm, p, &map_k, &map_q, meta, rank);
+        if (lane == 0) load_role(sm, p, &map_v, &map_r, &map_q, meta, rank);
     } else if (warp == 2) {
         value_role(sm, p, &map_v, meta, rank);
     } else if (warp == 1) {
@@ -635,7 +670,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const SharedPar
 
 size_t shared_smem_bytes() { return sizeof(shr::Smem); }
 
-cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
+cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_v, const CUtensorMap &map_r,
                           const CUtensorMap &map_q, cudaStream_t stream) {
     const size_t smem = shared_smem_bytes();
     cudaError_t e = cudaFuncSetAttribute(shr::shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -652,7 +687,7 @@ cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, shr::shared_kernel, map_k, map_v, map_q, p);
+    return cudaLaunchKernelEx(&cfg, shr::shared_kernel, map_v, map_r, map_q, p);
 }
 
 cudaError_t launch_shared_merge(const SharedParams &p, cudaStream_t stream) {
