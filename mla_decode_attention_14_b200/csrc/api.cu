@@ -31,7 +31,7 @@ cudaError_t launch_append(const __nv_bfloat16 *new_kv, int n_new, void *kv, int6
 cudaError_t launch_shared_metadata(const int32_t *seqlens, int batch, int groups, int prefix_units, int shared_blocks,
                                    int num_parts, int fixed_cost, int32_t *tile_meta, int32_t *num_splits,
                                    cudaStream_t stream);
-cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_v, const CUtensorMap &map_r,
+cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
                           const CUtensorMap &map_q, cudaStream_t stream);
 cudaError_t launch_shared_merge(const SharedParams &p, cudaStream_t stream);
 cudaError_t launch_rope_query(const rp::QueryParams &p, const mla_rope &rope, cudaStream_t stream);
@@ -596,9 +596,9 @@ int mla_decode_shared(const void *q, const void *kv_cache, int64_t num_blocks, c
     int rc = check_device();
     if (rc != MLA_OK) return rc;
     EncodeTiledFn enc = encode_fn();
-    CUtensorMap map_v, map_r, map_q;
-    if (!enc || !box_map(enc, &map_v, kv_cache, num_blocks * MLA_BLOCK_TOKENS, 4) ||
-        !box_map(enc, &map_r, kv_cache, num_blocks * MLA_BLOCK_TOKENS, 1) || !box_map(enc, &map_q, q, sh.total_rows, 9))
+    CUtensorMap map_k, map_v, map_q;
+    if (!enc || !box_map(enc, &map_k, kv_cache, num_blocks * MLA_BLOCK_TOKENS, 3) ||
+        !box_map(enc, &map_v, kv_cache, num_blocks * MLA_BLOCK_TOKENS, 4) || !box_map(enc, &map_q, q, sh.total_rows, 3))
         return MLA_ERR_CUDA;
     SharedParams p;
     p.shared_table = shared_table;
@@ -630,7 +630,7 @@ int mla_decode_shared(const void *q, const void *kv_cache, int64_t num_blocks, c
     // finite score can tell from it
     p.scale_log2 = std::fmax(scale * 1.4426950408889634f, 1e-37f);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_shared(p, map_v, map_r, map_q, st);
+    cudaError_t e = launch_shared(p, map_k, map_v, map_q, st);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     if (e != cudaSuccess) return cuda_status(e);
     e = launch_shared_merge(p, st);

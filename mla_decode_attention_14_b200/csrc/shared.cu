@@ -22,20 +22,23 @@
 //    (lane l: row l % 64; lanes 64-127 hold the upper half of the columns): O takes 256 columns and the
 //    scores of 128 tokens 64, so two score buffers fit beside it and no partial score or probability
 //    ever crosses between the SMs.
-//  * A tile is two cache blocks; CTA h loads block h whole (73,728 bytes, one TMA operation; K-major
-//    boxes of 64 tokens x 64 dims): its half of Gemm1's B operand. S = Q K^T: 36 MMAs of 128 x 128 x 16.
-//  * O += P V: 16 MMAs of 128 x 256 x 16 (MN-major B). CTA h provides value dims [256h, 256h + 256) of
-//    all 128 tokens: of its own block in place, of the other block loaded once more (32,768 bytes, from L2)
-//    over boxes that Gemm1 has finished with -- boxes 4-7 of CTA 0, 0-3 of CTA 1, so that the two
-//    CTAs' operands sit at the same offsets, as one descriptor needs. P (bf16) of block 0 goes over the
-//    dead rotary box, of block 1 into 8 KB of its own: two 128-token stages and Q fit in 227 KB.
+//  * A tile is two cache blocks. S = Q K^T: 36 MMAs of 128 x 128 x 16 (K-major boxes of 64 tokens x 64 dims);
+//    CTA h provides the tokens of block h, all 576 dims of it. O += P V: 16 MMAs of 128 x 256 x 16 (MN-major
+//    boxes); CTA h provides value dims [256h, 256h + 256) of both blocks. The two operands overlap only in
+//    part, and V is loaded on its own (from L2, where K has just put it), so that K's boxes are free as soon
+//    as Gemm1 has read them: K (9 boxes), V (8) and Q (9) have one buffer each, refilled in groups behind the
+//    MMAs, and every load has about a tile's time to land. (Keeping K for Gemm2 moves a quarter less into
+//    shared memory but holds a stage through the softmax: 173 us against 13x us with 128 heads, 128
+//    sequences and 4096 shared tokens.)
+//  * One warp of the leader issues QK(g + 1) before PV(g), so the tensor cores work through the softmax of a
+//    tile. Shared-memory bandwidth bounds the rest: 240 KB of operands read, 138 KB loaded and 16 KB of P
+//    written per tile and CTA, 3,080 cycles at 128 bytes per cycle, against 2,176 of the MMAs.
 //  * Eight softmax warps, one thread per (row, 32 tokens); the four threads of a row agree on the running
 //    maximum through shared memory, O is rescaled only when it grows by more than 2^8 (P <= 2^8, exact
-//    in the fp32 sums). P is rounded to bf16 once (to nearest): an error of at most 2^-9 of each term,
-//    the size of the output's own rounding, where a second term would add half to the MMA time.
-//  * Roles: warp 0 = K and Q loads; warp 2 = the other block's value half, zeroing of rows past the
-//    unit's end (undefined contents must not meet a zero probability); warps 1 and 3 of the leader
-//    issue Gemm1 and Gemm2; warps 4-11 softmax and epilogue.
+//    in the fp32 sums). P is rounded to bf16 once (to nearest): an error of at most 2^-8 of each term, the
+//    size of the output's own rounding, where a second term would add half to the MMA time.
+//  * Roles: warp 0 = loads; warp 1 of the leader = MMAs; warp 2 = zeroing of value rows past the unit's end
+//    (undefined contents must not meet a zero probability); warps 4-11 softmax and epilogue.
 // Every wait is bounded; a timeout sets the device error word and the pair exits cleanly.
 #include "pair_ptx.cuh"
 #include "shared.cuh"
@@ -46,26 +49,28 @@ using namespace sm100;
 namespace shr {
 constexpr int kTileTok = kSharedTileTok;       // 128 tokens: one cache block per CTA
 constexpr int kSoftWarps = 8, kThreads = 32 * (4 + kSoftWarps);
-constexpr int kStages = 2;
+constexpr int kGroups = 3;                     // of K's and Q's boxes
 constexpr int kBox = kBlk * 128;               // 64 rows x 64 bf16, 128-byte swizzle
 constexpr int kBoxes = kDqk / 64;              // 9
-constexpr int kStageBytes = kBoxes * kBox;     // 73,728: one cache block, or 64 query rows
-constexpr int kOtherBytes = 4 * kBox;          // the other block's 256 value dims
+constexpr int kGroupBoxes = kBoxes / kGroups;  // 3
+constexpr int kGroupBytes = kGroupBoxes * kBox;
+constexpr int kValueBytes = 4 * kBox;          // 256 value dims of one block
 constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemSCols = 64, kTmemCols = 512;
 
 struct __align__(1024) Smem {
-    uint8_t q[kStageBytes];
-    uint8_t stage[kStages][kStageBytes];
-    uint8_t p1[kBox];                          // P of the tile's second block (the first's: the rotary box)
+    uint8_t q[kBoxes * kBox];                  // this CTA's 64 query rows
+    uint8_t k[kBoxes * kBox];                  // its cache block of the tile
+    uint8_t v[2][kValueBytes];                 // its value dims of the tile's two blocks
+    uint8_t p[2][kBox];                        // P of its 64 rows, per block
     float xmax[2][4][64];                      // block maxima of a row's four threads; their sums at the end
-    // leader's, completed by both CTAs' loads: a tile's boxes 0-3 and 8, its boxes 4-7, Q, the value halves
-    uint64_t ka_full[kStages], kb_full[kStages], q_full, v_full[kStages];
-    // a piece's last, partial tile instead: this CTA's value half; both CTAs' after zeroing (leader's)
+    // leader's, completed by both CTAs' loads: a group of K (and, on a piece's first tile, of Q); a block of V
+    uint64_t k_full[kGroups], v_full[2];
+    // a unit's last, partial tile instead: this CTA's V; both CTAs' after zeroing (leader's)
     uint64_t tail_full, tail_ready;
-    uint64_t p_full[kStages];     // leader's: both CTAs' softmax warps
-    // commits to both CTAs: Gemm1; Gemm2 over the tile's first block; over both
-    uint64_t s_full[kStages], pv_half[kStages], pv_done[kStages];
+    uint64_t p_full;                           // leader's: both CTAs' softmax warps
+    // commits to both CTAs: Gemm1 has read a group; S is complete; Gemm2 has read a block of V (and P)
+    uint64_t k_free[kGroups], s_full[2], v_free[2];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
@@ -164,55 +169,88 @@ __device__ __forceinline__ int block_row(const SharedParams &p, const Piece &pc,
     return phys * kBlk;
 }
 
-// Before the pair exits: the loads of a barrier's fill have landed (bounded; independent of the abort flag).
-__device__ void landed(uint64_t *bar, int fill) {
-    const long long t0 = clock64();
-    while (!mbar_sleep_test(bar, fill & 1) && clock64() - t0 < kSpinCycles) {
-    }
-}
+// ---------------------------------------------------------------- warp 0, one thread: loads
+// In the order of use: K(g) (and Q), then V(g - 1).
+struct Loader {
+    Smem &sm;
+    const SharedParams &p;
+    const CUtensorMap *map_k, *map_v, *map_q;
+    uint32_t rank;
+    uint64_t pol_shared, pol_own;
+    int k_fills, v_fills, tails;  // groups and blocks issued; partial tiles among them
+    bool bad;
 
-// ---------------------------------------------------------------- warp 0, one thread: K tiles and Q
-__device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_v, const CUtensorMap *map_r,
-                          const CUtensorMap *map_q, const int32_t *meta, uint32_t rank) {
-    const uint64_t pol_shared = l2_evict_normal_policy(), pol_own = l2_evict_first_policy();
-    Walker w;
-    w.init(meta, p);
-    bool bad = false;
-    int g = 0, g_b = 0, pieces = 0;  // loads issued: first parts of tiles, second parts, queries
-    for (; w.live; w.advance(p)) {
-        const int s = g % kStages;
-        const uint32_t ph = (g / kStages - 1) & 1;
+    __device__ bool load_k(const Walker &w, int g) {
         const int blk = w.blk() + (int)rank;
         const int y = block_row(p, w.pc, blk, bad);
         const uint64_t pol = blk < p.shared_blocks ? pol_shared : pol_own;
-        // boxes 0-3 and 8 are free once Gemm2 has taken the tile's first block, the others after the second
-        if (g >= kStages && !mbar_poll(&sm.pv_half[s], ph, &sm.abort)) break;
-        if (rank == 0) mbar_arrive_expect_tx(&sm.ka_full[s], 2 * 5 * kBox);
-        const uint32_t ka = map_to_rank(&sm.ka_full[s], 0), kb = map_to_rank(&sm.kb_full[s], 0);
-        tma_load_3d_pair(sm.stage[s], map_v, 0, y, 0, ka, pol);
-        tma_load_3d_pair(sm.stage[s] + 8 * kBox, map_r, 0, y, 8, ka, pol);
-        ++g;
-        if (g > kStages && !mbar_poll(&sm.pv_done[s], ph, &sm.abort)) break;
-        if (rank == 0) mbar_arrive_expect_tx(&sm.kb_full[s], 2 * kOtherBytes);
-        tma_load_3d_pair(sm.stage[s] + 4 * kBox, map_v, 0, y, 4, kb, pol);
-        ++g_b;
-        if (w.first()) {  // Q follows once Gemm1 of the previous piece's last tile has read the old one
-            if (g > 1 && !mbar_poll(&sm.s_full[(g - 2) % kStages], ((g - 2) / kStages) & 1, &sm.abort)) break;
-            if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kStageBytes);
-            tma_load_3d_pair(sm.q, map_q, 0, w.q_row(p, (int)rank), 0, map_to_rank(&sm.q_full, 0), pol_own);
-            ++pieces;
+        const bool first = w.first();
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            if (g > 0 && !mbar_poll(&sm.k_free[i], (g - 1) & 1, &sm.abort)) return false;
+            const uint32_t bar = map_to_rank(&sm.k_full[i], 0);
+            if (rank == 0) mbar_arrive_expect_tx(&sm.k_full[i], (first ? 4 : 2) * kGroupBytes);
+            tma_load_3d_pair(sm.k + i * kGroupBytes, map_k, 0, y, kGroupBoxes * i, bar, pol);
+            if (first)
+                tma_load_3d_pair(sm.q + i * kGroupBytes, map_q, 0, w.q_row(p, (int)rank), kGroupBoxes * i, bar, pol_own);
+            ++k_fills;
         }
+        return true;
     }
-    if (bad) raise_error(kErrBounds);
-    // loads still in flight must land before the pair exits (the leader's barriers see both CTAs' loads)
-    if (rank == 0) {
-        for (int k = max(0, g - kStages); k < g; ++k) landed(&sm.ka_full[k % kStages], k / kStages);
-        for (int k = max(0, g_b - kStages); k < g_b; ++k) landed(&sm.kb_full[k % kStages], k / kStages);
-        if (pieces > 0) landed(&sm.q_full, pieces - 1);
+    __device__ bool load_v(const Walker &w, int g) {
+        const bool tail = w.tail();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (g > 0 && !mbar_poll(&sm.v_free[t], (g - 1) & 1, &sm.abort)) return false;
+            const int y = block_row(p, w.pc, w.blk() + t, bad);
+            if (!tail) {
+                if (rank == 0) mbar_arrive_expect_tx(&sm.v_full[t], 2 * kValueBytes);
+                tma_load_3d_pair(sm.v[t], map_v, 0, y, 4 * (int)rank, map_to_rank(&sm.v_full[t], 0), pol_own);
+            } else {
+                if (rank == 0) mbar_arrive(&sm.v_full[t]);  // keeps the phases in step
+                if (t == 0) mbar_arrive_expect_tx(&sm.tail_full, 2 * kValueBytes);
+                tma_load_3d(sm.v[t], map_v, 0, y, 4 * (int)rank, &sm.tail_full, pol_own);
+            }
+            ++v_fills;
+        }
+        tails += tail;
+        return true;
+    }
+};
+
+// Before the pair exits: fill number `fills` of a barrier's buffer has landed (bounded; independent of
+// the abort flag).
+__device__ void landed(uint64_t *bar, int fills) {
+    const long long t0 = clock64();
+    while (fills > 0 && !mbar_sleep_test(bar, (fills - 1) & 1) && clock64() - t0 < kSpinCycles) {
     }
 }
 
-// Zero this CTA's value rows past the unit's end in one block of the tile (its 4 boxes).
+__device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_k, const CUtensorMap *map_v,
+                          const CUtensorMap *map_q, const int32_t *meta, uint32_t rank) {
+    Loader ld{sm, p, map_k, map_v, map_q, rank, l2_evict_normal_policy(), l2_evict_first_policy(), 0, 0, 0, false};
+    Walker w, wv;  // of K, and one tile behind, of V
+    w.init(meta, p);
+    wv = w;
+    bool ok = true;
+    int g = 0;
+    for (; ok && w.live; w.advance(p), ++g) {
+        ok = ld.load_k(w, g);
+        if (ok && g > 0) {
+            ok = ld.load_v(wv, g - 1);
+            wv.advance(p);
+        }
+    }
+    if (ok && g > 0) ld.load_v(wv, g - 1);
+    if (ld.bad) raise_error(kErrBounds);
+    if (rank == 0) {  // the leader's barriers see both CTAs' loads
+        for (int i = 0; i < kGroups; ++i) landed(&sm.k_full[i], (ld.k_fills + kGroups - 1 - i) / kGroups);
+        for (int t = 0; t < 2; ++t) landed(&sm.v_full[t], (ld.v_fills + 1 - t) / 2);
+    }
+    landed(&sm.tail_full, ld.tails);
+}
+
+// Zero this CTA's value rows past the unit's end in one block of the tile (4 boxes).
 __device__ void zero_rows(uint8_t *boxes, int valid, int lane) {
     const uint4 z = make_uint4(0, 0, 0, 0);
     for (int e = lane; e < (kBlk - valid) * 8; e += 32) {
@@ -222,125 +260,94 @@ __device__ void zero_rows(uint8_t *boxes, int valid, int lane) {
     }
 }
 
-// ---------------------------------------------------------------- warp 2: the other block's value half
-__device__ void value_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_v, const int32_t *meta,
-                           uint32_t rank) {
-    const uint64_t policy = l2_evict_normal_policy();
+// ---------------------------------------------------------------- warp 2: partial tiles
+__device__ void tail_role(Smem &sm, const SharedParams &p, const int32_t *meta) {
     const int lane = threadIdx.x & 31;
-    const int other = 1 - (int)rank;
     Walker w;
     w.init(meta, p);
-    bool bad = false;
-    int tails = 0, g = 0;
-    for (; w.live; w.advance(p), ++g) {
-        const int s = g % kStages;
-        const bool tail = w.tail();
-        const int y = block_row(p, w.pc, w.blk() + other, bad);
-        if (!warp_poll(&sm.s_full[s], (g / kStages) & 1, &sm.abort, lane)) break;  // Gemm1 has read the boxes
-        uint8_t *dst = sm.stage[s] + 4 * other * kBox;
-        if (!tail) {
-            if (lane == 0) {
-                if (rank == 0) mbar_arrive_expect_tx(&sm.v_full[s], 2 * kOtherBytes);
-                tma_load_3d_pair(dst, map_v, 0, y, 4 * (int)rank, map_to_rank(&sm.v_full[s], 0), policy);
-            }
-            __syncwarp();
-            continue;
-        }
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.tail_full, kOtherBytes);
-            tma_load_3d(dst, map_v, 0, y, 4 * (int)rank, &sm.tail_full, policy);
-            if (rank == 0) mbar_arrive(&sm.v_full[s]);  // keeps the phases of the whole tiles' barrier in step
-        }
-        __syncwarp();
+    int tails = 0;
+    for (; w.live; w.advance(p)) {
+        if (!w.tail()) continue;
         if (!warp_poll(&sm.tail_full, tails & 1, &sm.abort, lane)) break;
         ++tails;
         const int left = w.pc.end_tok - w.blk() * kBlk;  // tokens of the tile (a missing block is zeros)
-        if (left < kBlk) zero_rows(sm.stage[s], max(left, 0), lane);
-        if (left > kBlk && left < kTileTok) zero_rows(sm.stage[s] + 4 * kBox, left - kBlk, lane);
+        if (left < kBlk) zero_rows(sm.v[0], max(left, 0), lane);
+        if (left > kBlk) zero_rows(sm.v[1], left - kBlk, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(map_to_rank(&sm.tail_ready, 0));
         __syncwarp();
     }
-    if (rank == 0 && lane == 0)
-        for (int k = max(0, g - kStages); k < g; ++k) landed(&sm.v_full[k % kStages], k / kStages);
-    __syncwarp();
 }
 
-// ---------------------------------------------------------------- warps 1 and 3 of the leader: MMAs
-__device__ void gemm1_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem) {
-    constexpr uint32_t id = idesc_bf16_f32(128, 128, 0);
-    const int lane = threadIdx.x & 31;
-    const uint64_t qd = smem_desc(smem_addr(sm.q), 16, 1024, 2);
-    Walker w;
-    w.init(meta, p);
-    for (int g = 0; w.live; w.advance(p), ++g) {
-        const int s = g % kStages;
-        const uint32_t ph = (g / kStages) & 1;
-        const uint64_t kd = smem_desc(smem_addr(sm.stage[s]), 16, 1024, 2);
-        const uint32_t d = tmem + kTmemS + kTmemSCols * s;
-        // the score buffer is free: K of this tile was loaded after Gemm2 of tile g - 2, which needed its P
-        if (w.first() && !warp_poll(&sm.q_full, w.piece_k & 1, &sm.abort, lane)) break;
-        if (!warp_poll(&sm.ka_full[s], ph, &sm.abort, lane)) break;
-        tc_fence_after();
-        if (elect_one()) {  // boxes 0-3 and 8, while the others land
+// ---------------------------------------------------------------- warp 1 of the leader: MMAs
+struct Issuer {
+    Smem &sm;
+    uint32_t tmem;
+    int lane, tails;
+
+    // S(g) = Q K^T. The score buffer is free: P of tile g - 2 was awaited before this.
+    __device__ bool scores(int g) {
+        constexpr uint32_t id = idesc_bf16_f32(128, 128, 0);
+        const uint64_t qd = smem_desc(smem_addr(sm.q), 16, 1024, 2), kd = smem_desc(smem_addr(sm.k), 16, 1024, 2);
+        const uint32_t d = tmem + kTmemS + kTmemSCols * (g & 1);
 #pragma unroll
-            for (int k = 0; k < 20; ++k) {
-                const int box = k < 16 ? k >> 2 : 8;
-                const uint64_t off = (uint64_t)((box * kBox + (k & 3) * 32) >> 4);
-                mma_ss_pair(d, qd + off, kd + off, id, k > 0 ? 1u : 0u);
-            }
-        }
-        __syncwarp();
-        if (!warp_poll(&sm.kb_full[s], ph, &sm.abort, lane)) break;
-        tc_fence_after();
-        if (elect_one()) {
+        for (int i = 0; i < kGroups; ++i) {
+            if (!warp_poll(&sm.k_full[i], g & 1, &sm.abort, lane)) return false;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 16; k < 32; ++k) {
-                const uint64_t off = (uint64_t)(((k >> 2) * kBox + (k & 3) * 32) >> 4);
-                mma_ss_pair(d, qd + off, kd + off, id, 1u);
+                for (int k = 0; k < 4 * kGroupBoxes; ++k) {
+                    const uint64_t off = (uint64_t)(((i * kGroupBoxes + (k >> 2)) * kBox + (k & 3) * 32) >> 4);
+                    mma_ss_pair(d, qd + off, kd + off, id, i + k > 0 ? 1u : 0u);
+                }
+                mma_commit_pair(&sm.k_free[i]);
+                if (i == kGroups - 1) mma_commit_pair(&sm.s_full[g & 1]);
             }
-            mma_commit_pair(&sm.s_full[s]);
+            __syncwarp();
         }
-        __syncwarp();
+        return true;
     }
-}
+    // O (+)= P V of tile g
+    __device__ bool values(int g, bool first, bool tail) {
+        constexpr uint32_t id = idesc_bf16_f32(128, 256, 1);  // MN-major B
+        const uint64_t pd = smem_desc(smem_addr(sm.p), 16, 1024, 2), vd = smem_desc(smem_addr(sm.v), kBox, 1024, 2);
+        if (!warp_poll(&sm.p_full, g & 1, &sm.abort, lane)) return false;
+        if (tail && !warp_poll(&sm.tail_ready, tails & 1, &sm.abort, lane)) return false;
+        tails += tail;
+        const uint32_t acc0 = first ? 0u : 1u;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (!tail && !warp_poll(&sm.v_full[t], g & 1, &sm.abort, lane)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // 16 tokens each
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)  // 128 value dims of each CTA
+                        mma_ss_pair(tmem + kTmemO + 128 * n, pd + (uint64_t)((t * kBox + k * 32) >> 4),
+                                    vd + (uint64_t)((t * kValueBytes + 2 * n * kBox + k * 2048) >> 4), id,
+                                    t + k > 0 ? 1u : acc0);
+                mma_commit_pair(&sm.v_free[t]);
+            }
+            __syncwarp();
+        }
+        return true;
+    }
+};
 
-__device__ void gemm2_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem) {
-    constexpr uint32_t id = idesc_bf16_f32(128, 256, 1);  // MN-major B
-    const int lane = threadIdx.x & 31;
-    const uint64_t p1d = smem_desc(smem_addr(sm.p1), 16, 1024, 2);
+__device__ void mma_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem) {
+    Issuer is{sm, tmem, (int)(threadIdx.x & 31), 0};
     Walker w;
     w.init(meta, p);
-    int tails = 0;
-    for (int g = 0; w.live; w.advance(p), ++g) {
-        const int s = g % kStages;
-        const uint32_t ph = (g / kStages) & 1;
-        if (w.tail()) {
-            if (!warp_poll(&sm.tail_ready, tails & 1, &sm.abort, lane)) break;
-            ++tails;
-        } else if (!warp_poll(&sm.v_full[s], ph, &sm.abort, lane)) {
-            break;
-        }
-        if (!warp_poll(&sm.p_full[s], ph, &sm.abort, lane)) break;
-        tc_fence_after();
-        const uint64_t p0d = smem_desc(smem_addr(sm.stage[s] + 8 * kBox), 16, 1024, 2);
-        const uint64_t vd = smem_desc(smem_addr(sm.stage[s]), kBox, 1024, 2);
-        const uint32_t acc0 = w.first() ? 0u : 1u;
-        if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {  // 16 tokens each; block t = k / 4
-                const uint64_t a = (k < 4 ? p0d : p1d) + 2 * (k & 3);
-                const uint64_t b = vd + (uint64_t)(((k >> 2) * 4 * kBox + (k & 3) * 2048) >> 4);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)  // 128 value dims of each CTA
-                    mma_ss_pair(tmem + kTmemO + 128 * n, a, b + (uint64_t)((2 * n * kBox) >> 4), id,
-                                k > 0 ? 1u : acc0);
-                if (k == 3) mma_commit_pair(&sm.pv_half[s]);
-            }
-            mma_commit_pair(&sm.pv_done[s]);
-        }
-        __syncwarp();
+    bool first = false, tail = false;  // of the tile before
+    for (int g = 0;; ++g) {
+        if (w.live && !is.scores(g)) break;
+        if (g > 0 && !is.values(g - 1, first, tail)) break;
+        if (!w.live) break;
+        first = w.first();
+        tail = w.tail();
+        w.advance(p);
     }
 }
 
@@ -366,7 +373,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
     const int x = 2 * blk + th;          // this thread's place among the row's four
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const float sl2 = p.scale_log2;
-    const uint32_t p_full0 = map_to_rank(&sm.p_full[0], 0), p_full1 = map_to_rank(&sm.p_full[1], 0);
+    const uint32_t p_full = map_to_rank(&sm.p_full, 0);
     // After a failed wait the warp walks on without waiting, so that no named barrier misses it.
     bool dead = false;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -378,8 +385,6 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
     int vis = 0, flat = 0;
     bool row_ok = false;
     for (int g = 0; w.live; ++g) {
-        const int s = g % kStages;
-        const uint32_t ph = (g / kStages) & 1;
         const bool first = w.first();
         if (first) {  // this row's visible keys within the piece
             flat = w.q_row(p, (int)rank) + i;
@@ -390,10 +395,10 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
             vis = min(vis, min(w.pc.first_blk + 2 * w.pc.hi, w.pc.end_blk) * kBlk);
         }
         const int key0 = w.blk() * kBlk + blk * kBlk + 32 * th;
-        wait(&sm.s_full[s], ph);
+        wait(&sm.s_full[g & 1], (g >> 1) & 1);
         tc_fence_after();
         uint32_t raw[32];
-        tmem_ld32(tmem + kTmemS + kTmemSCols * s + lane_off + 32 * th, raw);
+        tmem_ld32(tmem + kTmemS + kTmemSCols * (g & 1) + lane_off + 32 * th, raw);
         tmem_wait_ld();
         float v[32];
 #pragma unroll
@@ -439,8 +444,8 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
             unpack2(add2(add2(su[0], su[1]), add2(su[2], su[3])), a, b);
             l += a + b;
         }
-        // Gemm2 of the previous tile is done with P's second box and with O
-        if (g > 0) wait(&sm.pv_done[(g - 1) % kStages], ((g - 1) / kStages) & 1);
+        // Gemm2 of the previous tile is done with P and O
+        if (g > 0) wait(&sm.v_free[1], (g - 1) & 1);
         if (__any_sync(0xffffffffu, need)) {
             tc_fence_after();
 #pragma unroll 1
@@ -454,7 +459,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
             }
             tmem_wait_st();
         }
-        uint8_t *prow = (blk == 0 ? sm.stage[s] + 8 * kBox : sm.p1) + i * 128;
+        uint8_t *prow = sm.p[blk] + i * 128;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             *reinterpret_cast<uint4 *>(prow + (((4 * th + c) ^ (i & 7)) << 4)) =
@@ -462,7 +467,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(s == 0 ? p_full0 : p_full1);
+        if (lane == 0) mbar_arrive_pair(p_full);
 
         if (w.last()) {
             // the row's four sums, through the maxima's slots of the other parity (read before the barrier above)
@@ -476,7 +481,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
             const float lse2 = empty ? -INFINITY : m_ref + log2f(lr);
             const bool whole = p.prefix_units == 0 && w.pc.nsplit == 1;
             const int64_t part_row = w.pc.part_row + (int)rank * 64 + i;
-            wait(&sm.pv_done[s], ph);
+            wait(&sm.v_free[1], g & 1);
             tc_fence_after();
             const int col = 256 * blk + 128 * th;
 #pragma unroll 1
@@ -524,7 +529,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-shared_kernel(const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_r,
+shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
               const __grid_constant__ CUtensorMap map_q, const SharedParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of it is used: no room to align by hand
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -538,23 +543,23 @@ shared_kernel(const __grid_constant__ CUtensorMap map_v, const __grid_constant__
 
     if (warp == 1) tmem_alloc_pair(&sm.tmem_base, kTmemCols);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.ka_full[s], 1);
-            mbar_init(&sm.kb_full[s], 1);
-            mbar_init(&sm.v_full[s], 1);
-            mbar_init(&sm.p_full[s], 2 * kSoftWarps);
-            mbar_init(&sm.s_full[s], 1);
-            mbar_init(&sm.pv_half[s], 1);
-            mbar_init(&sm.pv_done[s], 1);
+        for (int i = 0; i < kGroups; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_free[i], 1);
         }
-        mbar_init(&sm.q_full, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sm.v_full[t], 1);
+            mbar_init(&sm.v_free[t], 1);
+            mbar_init(&sm.s_full[t], 1);
+        }
         mbar_init(&sm.tail_full, 1);
         mbar_init(&sm.tail_ready, 2);
-        mbar_init(&sm.mma_done, 2);
+        mbar_init(&sm.p_full, 2 * kSoftWarps);
+        mbar_init(&sm.mma_done, 1);
         sm.abort = 0;
         fence_mbar_init();
+        prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
-        prefetch_tensormap(&map_r);
         prefetch_tensormap(&map_q);
     }
     tc_fence_before();
@@ -564,19 +569,16 @@ shared_kernel(const __grid_constant__ CUtensorMap map_v, const __grid_constant__
     const uint32_t tmem = sm.tmem_base;
 
     if (warp == 0) {
-        if (lane == 0) load_role(sm, p, &map_v, &map_r, &map_q, meta, rank);
-    } else if (warp == 2) {
-        value_role(sm, p, &map_v, meta, rank);
+        if (lane == 0) load_role(sm, p, &map_k, &map_v, &map_q, meta, rank);
     } else if (warp == 1) {
         if (rank == 0) {
-            gemm1_role(sm, p, meta, tmem);
+            mma_role(sm, p, meta, tmem);
             drain_mmas(sm);
         }
+    } else if (warp == 2) {
+        tail_role(sm, p, meta);
     } else if (warp == 3) {
-        if (rank == 0) {
-            gemm2_role(sm, p, meta, tmem);
-            drain_mmas(sm);
-        }
+        // no work
     } else {
         softmax_role(sm, p, meta, tmem, rank);
     }
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const SharedPar
 
 size_t shared_smem_bytes() { return sizeof(shr::Smem); }
 
-cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_v, const CUtensorMap &map_r,
+cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
                           const CUtensorMap &map_q, cudaStream_t stream) {
     const size_t smem = shared_smem_bytes();
     cudaError_t e = cudaFuncSetAttribute(shr::shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -687,7 +689,7 @@ cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_v, const
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, shr::shared_kernel, map_v, map_r, map_q, p);
+    return cudaLaunchKernelEx(&cfg, shr::shared_kernel, map_k, map_v, map_q, p);
 }
 
 cudaError_t launch_shared_merge(const SharedParams &p, cudaStream_t stream) {
