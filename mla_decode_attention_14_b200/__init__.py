@@ -16,7 +16,6 @@ lse fp32 [b, h_q, s_q].
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -401,20 +400,36 @@ def absorb_o(o_latent: torch.Tensor, w_uv: torch.Tensor, out: torch.Tensor | Non
     return head_gemm(o_latent, h * D_V, D_V, w_uv, out, h * d, d, b * s_q, d, D_V, h, stream)
 
 
-def _on(dev: torch.device):
-    """Makes ``dev`` the current device for a call (nothing to do when it is)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+# The calls below take a few microseconds on the GPU at their smallest, so their host side is kept short: one
+# expression checks an argument, and _refuse says what was wrong when it fails.
+
+# torch's own accessor of a device's current stream as an integer (the public one builds a Stream object)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _stream_on(dev: torch.device, stream) -> int:
-    """The stream a call on ``dev`` goes to: the caller's, else that device's current one."""
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+def _is(t, dtype, index, ndim) -> bool:
+    return t.dtype is dtype and t.get_device() == index and t.dim() == ndim and t.is_contiguous()
 
 
-def _same_device(dev: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+def _refuse(t, name, dtype, index, ndim=None):
+    """Raises for a tensor that is not a contiguous ``dtype`` tensor of ``ndim`` dims on GPU ``index``."""
+    _need(t, name, dtype, ndim)
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
+
+
+def _launch(name: str, index: int, stream, *args):
+    """Calls the library with ``args`` and the stream (the caller's, else the device's current one) on GPU ``index``."""
+    fn = getattr(lib(), name)
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, st)
+    if rc != MLA_OK:
+        raise MLAError(name, rc)
 
 
 def get_metadata_shared(seqlens: torch.Tensor, h_q: int, s_q: int, shared_blocks: int, num_parts: int | None = None,
@@ -432,10 +447,8 @@ def get_metadata_shared(seqlens: torch.Tensor, h_q: int, s_q: int, shared_blocks
         raise MLAError("mla_shared_units", 1)
     tm = torch.empty((num_parts, META_INTS), dtype=torch.int32, device=dev)
     ns = torch.empty((units + 1,), dtype=torch.int32, device=dev)
-    with _on(dev):
-        _check("mla_get_metadata_shared", lib().mla_get_metadata_shared(
-            seqlens.data_ptr(), b, s_q, h_q, shared_blocks, num_parts, fixed_cost, tm.data_ptr(), ns.data_ptr(),
-            _stream_on(dev, stream)))
+    _launch("mla_get_metadata_shared", dev.index, stream, seqlens.data_ptr(), b, s_q, h_q, shared_blocks, num_parts,
+            fixed_cost, tm.data_ptr(), ns.data_ptr())
     return SharedMetadata(tm, ns, num_parts, fixed_cost, h_q, s_q, 0, shared_blocks)
 
 
@@ -454,46 +467,49 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, shared_table: torch.T
     Returns ``(out bf16 [b, s_q, h_q, 512], lse fp32 [b, h_q, s_q])``, as :func:`decode` with tables that
     all begin with ``shared_table``.
     """
-    _need(q, "q", torch.bfloat16, 4)
-    _need(kv_cache, "kv_cache", torch.bfloat16)
-    _need(shared_table, "shared_table", torch.int32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seqlens, "seqlens", torch.int32, 1)
+    i = q.get_device()
+    if not (i >= 0 and _is(q, torch.bfloat16, i, 4)):
+        _refuse(q, "q", torch.bfloat16, i, 4)
     b, s_q, h_q, d = q.shape
-    shared_blocks, dev = shared_table.shape[0], q.device
-    if d != D_QK or kv_cache.dim() not in (3, 4) or kv_cache.shape[1] != BLOCK or kv_cache.shape[-1] != D_QK or \
-            kv_cache.numel() != kv_cache.shape[0] * BLOCK * D_QK:
+    kv_shape = kv_cache.shape
+    if kv_cache.dtype is not torch.bfloat16 or kv_cache.get_device() != i or not kv_cache.is_contiguous():
+        _refuse(kv_cache, "kv_cache", torch.bfloat16, i)
+    if d != D_QK or (kv_shape[1:] != (BLOCK, 1, D_QK) and kv_shape[1:] != (BLOCK, D_QK)):
         raise ValueError("q must be [b, s_q, h_q, 576] and kv_cache [num_blocks, 64, 1, 576]")
+    if not _is(shared_table, torch.int32, i, 1):
+        _refuse(shared_table, "shared_table", torch.int32, i, 1)
+    if not _is(block_table, torch.int32, i, 2):
+        _refuse(block_table, "block_table", torch.int32, i, 2)
+    if not _is(seqlens, torch.int32, i, 1):
+        _refuse(seqlens, "seqlens", torch.int32, i, 1)
     if block_table.shape[0] != b or seqlens.shape[0] != b:
         raise ValueError("batch mismatch between q, block_table and seqlens")
-    if not isinstance(meta, SharedMetadata) or (meta.h_q, meta.s_q, meta.shared_blocks) != (h_q, s_q, shared_blocks) or \
-            meta.num_splits.shape[0] != lib().mla_shared_units(b, s_q, h_q, shared_blocks) + 1:
+    L, shared_blocks = lib(), shared_table.shape[0]
+    if not isinstance(meta, SharedMetadata) or meta.h_q != h_q or meta.s_q != s_q or meta.shared_blocks != shared_blocks \
+            or meta.num_splits.shape[0] != L.mla_shared_units(b, s_q, h_q, shared_blocks) + 1:
         raise ValueError("metadata was computed for another shape (use get_metadata_shared)")
+    if meta.num_splits.get_device() != i:
+        raise ValueError("meta must be on cuda:%d" % i)
     if out is None:
-        out = torch.empty((b, s_q, h_q, D_V), dtype=torch.bfloat16, device=dev)
-    else:
-        _need(out, "out", torch.bfloat16, 4)
-        if out.shape != (b, s_q, h_q, D_V):
-            raise ValueError("out must be [b, s_q, h_q, 512]")
+        out = torch.empty((b, s_q, h_q, D_V), dtype=torch.bfloat16, device=q.device)
+    elif not _is(out, torch.bfloat16, i, 4) or out.shape != (b, s_q, h_q, D_V):
+        _refuse(out, "out", torch.bfloat16, i, 4)
+        raise ValueError("out must be [b, s_q, h_q, 512]")
     if lse is None:
-        lse = torch.empty((b, h_q, s_q), dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", torch.float32, 3)
-        if lse.shape != (b, h_q, s_q):
-            raise ValueError("lse must be [b, h_q, s_q]")
-    ws_bytes = lib().mla_shared_workspace_bytes(b, s_q, h_q, shared_blocks, meta.num_parts)
+        lse = torch.empty((b, h_q, s_q), dtype=torch.float32, device=q.device)
+    elif not _is(lse, torch.float32, i, 3) or lse.shape != (b, h_q, s_q):
+        _refuse(lse, "lse", torch.float32, i, 3)
+        raise ValueError("lse must be [b, h_q, s_q]")
+    ws_bytes = L.mla_shared_workspace_bytes(b, s_q, h_q, shared_blocks, meta.num_parts)
     if workspace is None:
-        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < ws_bytes:
-        raise ValueError("workspace must be a contiguous CUDA tensor of at least %d bytes" % ws_bytes)
-    _same_device(dev, kv_cache=kv_cache, shared_table=shared_table, block_table=block_table, seqlens=seqlens, out=out,
-                 lse=lse, workspace=workspace, meta=meta.tile_meta)
-    with _on(dev):
-        _check("mla_decode_shared", lib().mla_decode_shared(
-            q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], shared_table.data_ptr(), shared_blocks,
-            block_table.data_ptr(), block_table.shape[1], seqlens.data_ptr(), meta.tile_meta.data_ptr(),
+        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != i or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < ws_bytes:
+        raise ValueError("workspace must be a contiguous tensor of at least %d bytes on cuda:%d" % (ws_bytes, i))
+    _launch("mla_decode_shared", i, stream, q.data_ptr(), kv_cache.data_ptr(), kv_shape[0], shared_table.data_ptr(),
+            shared_blocks, block_table.data_ptr(), block_table.shape[1], seqlens.data_ptr(), meta.tile_meta.data_ptr(),
             meta.num_splits.data_ptr(), meta.num_parts, b, s_q, h_q, scale, 1 if causal else 0, out.data_ptr(),
-            lse.data_ptr(), workspace.data_ptr(), ws_bytes, _stream_on(dev, stream)))
+            lse.data_ptr(), workspace.data_ptr(), ws_bytes)
     return out, lse
 
 
@@ -529,20 +545,13 @@ def rope(base: float = 10000.0, interleaved: bool = True, factor: float = 1.0, o
     return Rope(c)
 
 
-def _row_strides(t: torch.Tensor, name: str, tokens_dims: int):
-    """(stride between tokens, between heads) of t[tokens..., heads, dims], in elements; 0 for a single one."""
-    if t.stride(-1) != 1:
-        raise ValueError("%s must have its last dim contiguous" % name)
-    sizes, strides = t.shape, t.stride()
-    if tokens_dims == 1:
-        ld = strides[0] if sizes[0] > 1 else 0
-    elif sizes[1] == 1:
-        ld = strides[0] if sizes[0] > 1 else 0
-    else:
-        ld = strides[1]
-        if sizes[0] > 1 and strides[0] != sizes[1] * ld:
-            raise ValueError("%s must have evenly spaced tokens" % name)
-    return ld, strides[-2] if sizes[-2] > 1 else 0
+def _token_stride(sizes, strides, name: str) -> int:
+    """Elements between the tokens of t[b, n, ...] (0 for a single token); raises if they are not evenly spaced."""
+    if sizes[1] == 1:
+        return strides[0] if sizes[0] > 1 else 0
+    if sizes[0] > 1 and strides[0] != sizes[1] * strides[1]:
+        raise ValueError("%s must have evenly spaced tokens" % name)
+    return strides[1]
 
 
 def rope_q(x: torch.Tensor, q: torch.Tensor, rope: Rope, seqlens: torch.Tensor | None = None,
@@ -554,89 +563,100 @@ def rope_q(x: torch.Tensor, q: torch.Tensor, rope: Rope, seqlens: torch.Tensor |
     with 576 dims. ``positions`` int32, one per token; without it (4-D only) token t of sequence b is at
     ``seqlens[b] + t``, seqlens int32 ``[b]`` being the lengths before the new tokens.
     """
-    nd = x.dim()
-    if x.dtype != torch.bfloat16 or q.dtype != torch.bfloat16:
+    xs, qs = x.shape, q.shape
+    i, nd = x.get_device(), len(xs)
+    if x.dtype is not torch.bfloat16 or q.dtype is not torch.bfloat16:
         raise TypeError("x and q must be bfloat16, got %s and %s" % (x.dtype, q.dtype))
-    if not x.is_cuda or not q.is_cuda:
-        raise ValueError("x and q must be CUDA tensors")
-    if nd not in (3, 4) or x.shape[-1] != D_QK - D_V or q.shape != x.shape[:-1] + (D_QK,):
+    if i < 0 or q.get_device() != i:
+        raise ValueError("x and q must be CUDA tensors on one device")
+    if (nd != 4 and nd != 3) or len(qs) != nd or xs[-1] != D_QK - D_V or qs[-1] != D_QK or xs[:-1] != qs[:-1]:
         raise ValueError("shapes: x [b, s_q, h, 64] and q [b, s_q, h, 576], or x [tokens, h, 64] and q [tokens, h, 576]")
-    dev = x.device
-    tokens, s_q = x.shape[0], 1
-    if nd == 4:
-        s_q = x.shape[1]
-        tokens *= s_q
+    s_q = xs[1] if nd == 4 else 1
+    tokens = xs[0] * s_q
     if positions is not None:
-        _need(positions, "positions", torch.int32)
+        if positions.dtype is not torch.int32 or positions.get_device() != i or not positions.is_contiguous():
+            _refuse(positions, "positions", torch.int32, i)
         if positions.numel() != tokens:
             raise ValueError("positions must hold one value per token")
+        at, seqlens = positions.data_ptr(), None
     elif nd == 3 or seqlens is None:
         raise ValueError("positions must be given for packed tokens; seqlens or positions otherwise")
     else:
-        _need(seqlens, "seqlens", torch.int32, 1)
-        if seqlens.shape[0] != x.shape[0]:
+        if not _is(seqlens, torch.int32, i, 1):
+            _refuse(seqlens, "seqlens", torch.int32, i, 1)
+        if seqlens.shape[0] != xs[0]:
             raise ValueError("batch mismatch between x and seqlens")
-    _same_device(dev, q=q, seqlens=seqlens, positions=positions)
-    if x.numel() == 0:
+        at, seqlens = None, seqlens.data_ptr()
+    heads = xs[-2]
+    if tokens == 0 or heads == 0:
         return q
-    ldx, hx = _row_strides(x, "x", nd - 2)
-    ldq, hq = _row_strides(q, "q", nd - 2)
-    with _on(dev):
-        _check("mla_rope_q", lib().mla_rope_q(
-            x.data_ptr(), ldx, hx, q.data_ptr() + 2 * D_V, ldq, hq, tokens, x.shape[-2],
-            None if positions is None else positions.data_ptr(),
-            None if positions is not None else seqlens.data_ptr(), s_q, rope.ref, _stream_on(dev, stream)))
+    st, sq = x.stride(), q.stride()
+    if st[-1] != 1 or sq[-1] != 1:
+        raise ValueError("x and q must have their last dim contiguous")
+    if nd == 4:
+        ldx, ldq = _token_stride(xs, st, "x"), _token_stride(qs, sq, "q")
+    else:
+        ldx, ldq = (st[0], sq[0]) if tokens > 1 else (0, 0)
+    hx, hq = (st[-2], sq[-2]) if heads > 1 else (0, 0)
+    _launch("mla_rope_q", i, stream, x.data_ptr(), ldx, hx, q.data_ptr() + 2 * D_V, ldq, hq, tokens, heads, at, seqlens,
+            s_q, rope.ref)
     return q
 
 
 def _append_rope(fp8, new_kv, kv_cache, block_table, seqlens, kv_scale, rope, norm_weight, eps, positions, cu_new, stream):
-    fn = "mla_append_kv_rope_fp8" if fp8 else "mla_append_kv_rope"
-    if new_kv.dtype != torch.bfloat16:
+    i, b, width = new_kv.get_device(), seqlens.shape[0], FP8_RECORD_BYTES if fp8 else D_QK
+    if new_kv.dtype is not torch.bfloat16:
         raise TypeError("new_kv must be bfloat16, got %s" % new_kv.dtype)
-    if not new_kv.is_cuda:
+    if i < 0:
         raise ValueError("new_kv must be a CUDA tensor")
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seqlens, "seqlens", torch.int32, 1)
-    _need(kv_cache, "kv_cache", torch.uint8 if fp8 else torch.bfloat16)
-    dev, b, width = new_kv.device, seqlens.shape[0], FP8_RECORD_BYTES if fp8 else D_QK
-    if new_kv.shape[-1] != D_QK or new_kv.dim() != (3 if cu_new is None else 2):
-        raise ValueError("new_kv must be [b, n_new, 576], or [tokens, 576] with cu_new")
-    if kv_cache.dim() not in (3, 4) or kv_cache.shape[1] != BLOCK or kv_cache.shape[-1] != width or \
-            kv_cache.numel() != kv_cache.shape[0] * BLOCK * width:
+    if not _is(block_table, torch.int32, i, 2):
+        _refuse(block_table, "block_table", torch.int32, i, 2)
+    if not _is(seqlens, torch.int32, i, 1):
+        _refuse(seqlens, "seqlens", torch.int32, i, 1)
+    kv_dtype, kv_shape = torch.uint8 if fp8 else torch.bfloat16, kv_cache.shape
+    if kv_cache.dtype is not kv_dtype or kv_cache.get_device() != i or not kv_cache.is_contiguous():
+        _refuse(kv_cache, "kv_cache", kv_dtype, i)
+    if kv_shape[1:] != (BLOCK, 1, width) and kv_shape[1:] != (BLOCK, width):
         raise ValueError("the cache must be [num_blocks, 64, 1, %d]" % width)
     if block_table.shape[0] != b:
         raise ValueError("batch mismatch between block_table and seqlens")
+    xs, st = new_kv.shape, new_kv.stride()
+    if len(xs) != (3 if cu_new is None else 2) or xs[-1] != D_QK:
+        raise ValueError("new_kv must be [b, n_new, 576], or [tokens, 576] with cu_new")
+    if st[-1] != 1:
+        raise ValueError("new_kv must have its last dim contiguous")
     if cu_new is None:
-        if new_kv.shape[0] != b:
+        if xs[0] != b:
             raise ValueError("batch mismatch between new_kv and seqlens")
-        n_new = new_kv.shape[1]
-        tokens = b * n_new
+        n_new = xs[1]
+        tokens, cu = b * n_new, None
+        ld = _token_stride(xs, st, "new_kv") if tokens else 0
     else:
-        _need(cu_new, "cu_new", torch.int32, 1)
+        if not _is(cu_new, torch.int32, i, 1):
+            _refuse(cu_new, "cu_new", torch.int32, i, 1)
         if cu_new.shape[0] != b + 1:
             raise ValueError("cu_new must hold b + 1 values")
-        tokens, n_new = new_kv.shape[0], 0
+        tokens, n_new, cu, ld = xs[0], 0, cu_new.data_ptr(), st[0] if xs[0] > 1 else 0
+    weight = at = None
     if norm_weight is not None:
-        _need(norm_weight, "norm_weight", torch.bfloat16, 1)
-        if norm_weight.shape[0] != D_V:
+        if not _is(norm_weight, torch.bfloat16, i, 1) or norm_weight.shape[0] != D_V:
+            _refuse(norm_weight, "norm_weight", torch.bfloat16, i, 1)
             raise ValueError("norm_weight must hold 512 values")
+        weight = norm_weight.data_ptr()
     if positions is not None:
-        _need(positions, "positions", torch.int32)
+        if positions.dtype is not torch.int32 or positions.get_device() != i or not positions.is_contiguous():
+            _refuse(positions, "positions", torch.int32, i)
         if positions.numel() != tokens:
             raise ValueError("positions must hold one value per token")
-    _same_device(dev, cache=kv_cache, block_table=block_table, seqlens=seqlens, cu_new=cu_new, norm_weight=norm_weight,
-                 positions=positions)
+        at = positions.data_ptr()
     if tokens == 0:
         return
-    # a row stands where a head does in _row_strides' layout: one of them per token
-    ld = _row_strides(new_kv.unsqueeze(-2), "new_kv", new_kv.dim() - 1)[0] or D_QK
-    scale = (kv_scale,) if fp8 else ()
-    with _on(dev):
-        _check(fn, getattr(lib(), fn)(
-            new_kv.data_ptr(), ld, tokens, n_new, None if cu_new is None else cu_new.data_ptr(),
-            None if norm_weight is None else norm_weight.data_ptr(), eps, rope.ref,
-            None if positions is None else positions.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], *scale,
-            block_table.data_ptr(), block_table.shape[1], seqlens.data_ptr(), b, _stream_on(dev, stream)))
+    head = (new_kv.data_ptr(), ld or D_QK, tokens, n_new, cu, weight, eps, rope.ref, at, kv_cache.data_ptr(), kv_shape[0])
+    tail = (block_table.data_ptr(), block_table.shape[1], seqlens.data_ptr(), b)
+    if fp8:
+        _launch("mla_append_kv_rope_fp8", i, stream, *head, kv_scale, *tail)
+    else:
+        _launch("mla_append_kv_rope", i, stream, *head, *tail)
 
 
 def append_kv_rope(new_kv: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor,

@@ -18,14 +18,13 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Bounded waits that poll instead of sleeping: a thread suspended on a barrier wakes up to about a
-// thousand cycles after the phase completes, which the short dependent steps of a pair kernel cannot
-// hide. One lane polls for its warp. Same contract as mbar_wait (false: *abort was set, or the bound
-// passed and *abort is now set).
+// Bounded waits without a suspend-time hint, by one lane for its warp: with one, a warp was seen to wake up
+// to about a thousand cycles after its phase, which the short dependent steps of a pair kernel cannot hide.
+// Same contract as mbar_wait (false: *abort was set, or the bound passed and *abort is now set).
 __device__ __forceinline__ bool mbar_poll_once(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
@@ -96,6 +95,11 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         " [%0], [%1, {%2, %3, %4}], [%5], %6;"
         ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
         : "memory");
+}
+// Brings a box into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
 }
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
     uint64_t p;

@@ -38,7 +38,8 @@
 //    in the fp32 sums). P is rounded to bf16 once (to nearest): an error of at most 2^-8 of each term, the
 //    size of the output's own rounding, where a second term would add half to the MMA time.
 //  * Roles: warp 0 = loads; warp 1 of the leader = MMAs; warp 2 = zeroing of value rows past the unit's end
-//    (undefined contents must not meet a zero probability); warps 4-11 softmax and epilogue.
+//    (undefined contents must not meet a zero probability); warp 3 = table look-ups ahead; warps 4-11 softmax
+//    and epilogue.
 // Every wait is bounded; a timeout sets the device error word and the pair exits cleanly.
 #include "pair_ptx.cuh"
 #include "shared.cuh"
@@ -55,6 +56,7 @@ constexpr int kBoxes = kDqk / 64;              // 9
 constexpr int kGroupBoxes = kBoxes / kGroups;  // 3
 constexpr int kGroupBytes = kGroupBoxes * kBox;
 constexpr int kValueBytes = 4 * kBox;          // 256 value dims of one block
+constexpr int kAhead = 4;                      // tiles whose cache rows are looked up before they are loaded
 constexpr float kRescaleThreshold = 8.0f;      // log2 units
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemSCols = 64, kTmemCols = 512;
 
@@ -72,6 +74,8 @@ struct __align__(1024) Smem {
     // commits to both CTAs: Gemm1 has read a group; S is complete; Gemm2 has read a block of V (and P)
     uint64_t k_free[kGroups], s_full[2], v_free[2];
     uint64_t mma_done;
+    uint64_t r_full[kAhead], r_free[kAhead];   // tiles whose cache rows are known; whose loads are issued
+    int row[kAhead][2];
     uint32_t tmem_base;
     int abort;
 };
@@ -178,16 +182,16 @@ struct Loader {
     uint32_t rank;
     uint64_t pol_shared, pol_own;
     int k_fills, v_fills, tails;  // groups and blocks issued; partial tiles among them
-    bool bad;
 
     __device__ bool load_k(const Walker &w, int g) {
         const int blk = w.blk() + (int)rank;
-        const int y = block_row(p, w.pc, blk, bad);
+        if (!mbar_wait(&sm.r_full[g % kAhead], (g / kAhead) & 1, &sm.abort)) return false;
+        const int y = *(volatile int *)&sm.row[g % kAhead][rank];
         const uint64_t pol = blk < p.shared_blocks ? pol_shared : pol_own;
         const bool first = w.first();
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            if (g > 0 && !mbar_poll(&sm.k_free[i], (g - 1) & 1, &sm.abort)) return false;
+            if (g > 0 && !mbar_wait(&sm.k_free[i], (g - 1) & 1, &sm.abort)) return false;
             const uint32_t bar = map_to_rank(&sm.k_full[i], 0);
             if (rank == 0) mbar_arrive_expect_tx(&sm.k_full[i], (first ? 4 : 2) * kGroupBytes);
             tma_load_3d_pair(sm.k + i * kGroupBytes, map_k, 0, y, kGroupBoxes * i, bar, pol);
@@ -201,8 +205,8 @@ struct Loader {
         const bool tail = w.tail();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (g > 0 && !mbar_poll(&sm.v_free[t], (g - 1) & 1, &sm.abort)) return false;
-            const int y = block_row(p, w.pc, w.blk() + t, bad);
+            if (g > 0 && !mbar_wait(&sm.v_free[t], (g - 1) & 1, &sm.abort)) return false;
+            const int y = *(volatile int *)&sm.row[g % kAhead][t];
             if (!tail) {
                 if (rank == 0) mbar_arrive_expect_tx(&sm.v_full[t], 2 * kValueBytes);
                 tma_load_3d_pair(sm.v[t], map_v, 0, y, 4 * (int)rank, map_to_rank(&sm.v_full[t], 0), pol_own);
@@ -214,6 +218,7 @@ struct Loader {
             ++v_fills;
         }
         tails += tail;
+        mbar_arrive(&sm.r_free[g % kAhead]);
         return true;
     }
 };
@@ -227,11 +232,9 @@ __device__ void landed(uint64_t *bar, int fills) {
 }
 
 __device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_k, const CUtensorMap *map_v,
-                          const CUtensorMap *map_q, const int32_t *meta, uint32_t rank) {
-    Loader ld{sm, p, map_k, map_v, map_q, rank, l2_evict_normal_policy(), l2_evict_first_policy(), 0, 0, 0, false};
-    Walker w, wv;  // of K, and one tile behind, of V
-    w.init(meta, p);
-    wv = w;
+                          const CUtensorMap *map_q, Walker w, uint32_t rank) {
+    Loader ld{sm, p, map_k, map_v, map_q, rank, l2_evict_normal_policy(), l2_evict_first_policy(), 0, 0, 0};
+    Walker wv = w;  // of V, one tile behind
     bool ok = true;
     int g = 0;
     for (; ok && w.live; w.advance(p), ++g) {
@@ -242,12 +245,35 @@ __device__ void load_role(Smem &sm, const SharedParams &p, const CUtensorMap *ma
         }
     }
     if (ok && g > 0) ld.load_v(wv, g - 1);
-    if (ld.bad) raise_error(kErrBounds);
     if (rank == 0) {  // the leader's barriers see both CTAs' loads
         for (int i = 0; i < kGroups; ++i) landed(&sm.k_full[i], (ld.k_fills + kGroups - 1 - i) / kGroups);
         for (int t = 0; t < 2; ++t) landed(&sm.v_full[t], (ld.v_fills + 1 - t) / 2);
     }
     landed(&sm.tail_full, ld.tails);
+}
+
+// ---------------------------------------------------------------- warp 3, one thread: cache rows ahead of the loads
+// A tile's blocks are found by dependent loads (unit, length, table), and contents that only one
+// sequence owns come from HBM: the rows are looked up kAhead tiles early and such blocks brought into L2.
+__device__ void resolve_role(Smem &sm, const SharedParams &p, const CUtensorMap *map_k, const CUtensorMap *map_q, Walker w,
+                             uint32_t rank) {
+    bool bad = false;
+    for (int g = 0; w.live; w.advance(p), ++g) {
+        const int s = g % kAhead;
+        const int y0 = block_row(p, w.pc, w.blk(), bad), y1 = block_row(p, w.pc, w.blk() + 1, bad);
+        if (g >= kAhead && !mbar_wait(&sm.r_free[s], (g / kAhead - 1) & 1, &sm.abort)) break;
+        *(volatile int *)&sm.row[s][0] = y0;
+        *(volatile int *)&sm.row[s][1] = y1;
+        mbar_arrive(&sm.r_full[s]);
+        if (g > 0 && w.first())
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) tma_prefetch_3d(map_q, 0, w.q_row(p, (int)rank), kGroupBoxes * i);
+        const int blk = w.blk() + (int)rank;
+        if (g > 0 && blk >= p.shared_blocks && blk < w.pc.end_blk)
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) tma_prefetch_3d(map_k, 0, rank == 0 ? y0 : y1, kGroupBoxes * i);
+    }
+    if (bad) raise_error(kErrBounds);
 }
 
 // Zero this CTA's value rows past the unit's end in one block of the tile (4 boxes).
@@ -261,10 +287,8 @@ __device__ void zero_rows(uint8_t *boxes, int valid, int lane) {
 }
 
 // ---------------------------------------------------------------- warp 2: partial tiles
-__device__ void tail_role(Smem &sm, const SharedParams &p, const int32_t *meta) {
+__device__ void tail_role(Smem &sm, const SharedParams &p, Walker w) {
     const int lane = threadIdx.x & 31;
-    Walker w;
-    w.init(meta, p);
     int tails = 0;
     for (; w.live; w.advance(p)) {
         if (!w.tail()) continue;
@@ -336,10 +360,8 @@ struct Issuer {
     }
 };
 
-__device__ void mma_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem) {
+__device__ void mma_role(Smem &sm, const SharedParams &p, Walker w, uint32_t tmem) {
     Issuer is{sm, tmem, (int)(threadIdx.x & 31), 0};
-    Walker w;
-    w.init(meta, p);
     bool first = false, tail = false;  // of the tile before
     for (int g = 0;; ++g) {
         if (w.live && !is.scores(g)) break;
@@ -365,7 +387,7 @@ __device__ void drain_mmas(Smem &sm) {
 // ---------------------------------------------------------------- warps 4-11: softmax and epilogue
 // Warp w: TMEM lane quarter w & 3 (rows 32 (w & 1) .. + 32 of the CTA's 64; block (w >> 1) & 1 of the tile),
 // 32 of that block's tokens (th). Of O, its lanes hold dims [256 blk + 128 th, + 128) of its rows.
-__device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *meta, uint32_t tmem, uint32_t rank) {
+__device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t tmem, uint32_t rank) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wq = warp & 3, blk = wq >> 1, th = (warp - 4) >> 2;
     const int i = (wq & 1) * 32 + lane;  // row of this CTA's 64
@@ -379,8 +401,6 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!dead && !warp_poll(bar, parity, &sm.abort, lane)) dead = true;
     };
-    Walker w;
-    w.init(meta, p);
     float m_ref = -INFINITY, l = 0.f;
     int vis = 0, flat = 0;
     bool row_ok = false;
@@ -528,7 +548,8 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, const int32_t *met
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// (bounds of 512 threads for 128 registers at most: 1% faster than the 149 that 384 would give)
+__global__ void __launch_bounds__(512, 1)
 shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
               const __grid_constant__ CUtensorMap map_q, const SharedParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of it is used: no room to align by hand
@@ -552,6 +573,10 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             mbar_init(&sm.v_free[t], 1);
             mbar_init(&sm.s_full[t], 1);
         }
+        for (int k = 0; k < kAhead; ++k) {
+            mbar_init(&sm.r_full[k], 1);
+            mbar_init(&sm.r_free[k], 1);
+        }
         mbar_init(&sm.tail_full, 1);
         mbar_init(&sm.tail_ready, 2);
         mbar_init(&sm.p_full, 2 * kSoftWarps);
@@ -562,6 +587,8 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         prefetch_tensormap(&map_v);
         prefetch_tensormap(&map_q);
     }
+    Walker w;
+    w.init(meta, p);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist
@@ -569,18 +596,18 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const uint32_t tmem = sm.tmem_base;
 
     if (warp == 0) {
-        if (lane == 0) load_role(sm, p, &map_k, &map_v, &map_q, meta, rank);
+        if (lane == 0) load_role(sm, p, &map_k, &map_v, &map_q, w, rank);
     } else if (warp == 1) {
         if (rank == 0) {
-            mma_role(sm, p, meta, tmem);
+            mma_role(sm, p, w, tmem);
             drain_mmas(sm);
         }
     } else if (warp == 2) {
-        tail_role(sm, p, meta);
+        tail_role(sm, p, w);
     } else if (warp == 3) {
-        // no work
+        if (lane == 0) resolve_role(sm, p, &map_k, &map_q, w, rank);
     } else {
-        softmax_role(sm, p, meta, tmem, rank);
+        softmax_role(sm, p, w, tmem, rank);
     }
     __syncwarp();
     tc_fence_before();
@@ -595,20 +622,28 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 }
 
 // ---------------------------------------------------------------- merging the pieces of a row
-// One warp per row: the pieces of its prefix unit, then those of its own unit; 16 dims per lane.
-constexpr int kMergeWarps = 8;
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const SharedParams p) {
-    const int flat = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+// Two warps per row, 8 dims per lane: the pieces of its prefix unit, then those of its own unit. Bound by
+// latency (a few dependent rounds of loads) and, for many rows, by the partials' bytes (2 KB a piece and
+// row, from L2): lane k reads the lse of piece k, four pieces' outputs are in flight per warp beside it.
+constexpr int kMergeWarps = 8, kMergeFly = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_kernel(const SharedParams p) {
+    const int64_t w = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    const int flat = (int)(w >> 1), lane = threadIdx.x & 31;
     if (flat >= p.total_rows) return;
+    const int d0 = (int)(w & 1) * (kDv / 2) + 8 * lane;
     const int seq = flat / p.rows, r = flat % p.rows;
-    const int pu = flat / 128, ou = p.prefix_units + seq * p.groups + r / 128;
+    const int ou = p.prefix_units + seq * p.groups + r / 128;
     const int o0 = p.num_splits[ou], no = p.num_splits[ou + 1] - o0;
-    const int p0 = p.prefix_units > 0 ? p.num_splits[pu] : 0, np = p.prefix_units > 0 ? p.num_splits[pu + 1] - p0 : 0;
-    const int ob = p.num_splits[p.prefix_units];
-    if (p.prefix_units == 0 && no == 1) return;  // written by the attention kernel
-    if (no < 0 || np < 0 || o0 < 0 || p0 < 0 || no + np > 2 * p.num_parts + 2 ||
-        o0 + no > p.units + p.num_parts || p0 + np > p.units + p.num_parts || o0 < ob) {  // malformed metadata
+    int p0 = 0, np = 0, ob = 0;
+    if (p.prefix_units > 0) {
+        p0 = p.num_splits[flat / 128];
+        np = p.num_splits[flat / 128 + 1] - p0;
+        ob = p.num_splits[p.prefix_units];
+    } else if (no == 1) {
+        return;  // written by the attention kernel
+    }
+    if (no < 0 || np < 0 || p0 < 0 || o0 < ob || p0 + np > p.prefix_units + p.num_parts ||
+        o0 - ob + no > p.units - p.prefix_units + p.num_parts) {  // malformed metadata
         if (lane == 0) raise_error(kErrBounds);
         return;
     }
@@ -616,55 +651,61 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const SharedPar
     const int64_t orow = p.own_base + (int64_t)(o0 - ob) * p.own_rows + r % 128;
     const int ns = np + no;
     const auto row_of = [&](int k) { return k < np ? prow + (int64_t)k * 128 : orow + (int64_t)(k - np) * p.own_rows; };
-    float m = -INFINITY;
-    for (int k = lane; k < ns; k += 32) m = fmaxf(m, p.lse_part[row_of(k)]);
+    float acc[8], m = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[16];
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    for (int base = 0; base < ns; base += 32) {
+        const int n = min(32, ns - base);
+        const float ls = lane < n ? p.lse_part[row_of(base + lane)] : -INFINITY;
+        float mx = m, wgt = 0.f, a = 1.f;
+        for (int k0 = 0; k0 < n; k0 += kMergeFly) {
+            float4 v[kMergeFly][2];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-    float sum = 0.f;
-    if (m != -INFINITY) {
-        for (int k0 = 0; k0 < ns; k0 += 4) {  // four pieces' loads in flight
-            float w[4];
-            float4 v[4][4];
+            for (int d = 0; d < kMergeFly; ++d) {
+                const float4 *src =
+                    reinterpret_cast<const float4 *>(p.o_part + (size_t)row_of(base + min(k0 + d, n - 1)) * kDv + d0);
+                v[d][0] = src[0];
+                v[d][1] = src[1];
+            }
+            if (k0 == 0) {  // the weights of these pieces, while the outputs arrive
+                mx = fmaxf(m, ls);
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const bool on = k0 + d < ns;
-                const int64_t row = row_of(on ? k0 + d : 0);
-                w[d] = on ? exp2f(p.lse_part[row] - m) : 0.f;
-                const float4 *src = reinterpret_cast<const float4 *>(p.o_part + (size_t)row * kDv + 16 * lane);
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                if (mx == -INFINITY) break;  // no key so far
+                wgt = exp2f(ls - mx);
+                a = exp2f(m - mx);
+                float s = wgt;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[d][j] = on ? src[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                sum = fmaf(sum, a, s);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] *= a;
+                m = mx;
             }
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                if (w[d] == 0.f) continue;  // no key in the piece, or a negligible weight
-                sum += w[d];
+            for (int d = 0; d < kMergeFly; ++d) {  // a piece without keys has zeros; past the last, weight 0
+                const float wd = __shfl_sync(0xffffffffu, wgt, min(k0 + d, 31));
+                const float u = k0 + d < n ? wd : 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[4 * j + 0] = fmaf(w[d], v[d][j].x, acc[4 * j + 0]);
-                    acc[4 * j + 1] = fmaf(w[d], v[d][j].y, acc[4 * j + 1]);
-                    acc[4 * j + 2] = fmaf(w[d], v[d][j].z, acc[4 * j + 2]);
-                    acc[4 * j + 3] = fmaf(w[d], v[d][j].w, acc[4 * j + 3]);
+                for (int j = 0; j < 2; ++j) {
+                    acc[4 * j + 0] = fmaf(u, v[d][j].x, acc[4 * j + 0]);
+                    acc[4 * j + 1] = fmaf(u, v[d][j].y, acc[4 * j + 1]);
+                    acc[4 * j + 2] = fmaf(u, v[d][j].z, acc[4 * j + 2]);
+                    acc[4 * j + 3] = fmaf(u, v[d][j].w, acc[4 * j + 3]);
                 }
             }
         }
-        const float inv = 1.f / sum;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) acc[j] *= inv;
     }
-    uint4 packed[2];
-    uint32_t *pw = reinterpret_cast<uint32_t *>(packed);
+    const float inv = m == -INFINITY ? 0.f : 1.f / sum;
+    uint4 packed;
+    uint32_t *pw = reinterpret_cast<uint32_t *>(&packed);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        __nv_bfloat162 two = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
+    for (int k = 0; k < 4; ++k) {
+        __nv_bfloat162 two = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
         pw[k] = *reinterpret_cast<uint32_t *>(&two);
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)flat * kDv + 16 * lane);
-    dst[0] = packed[0];
-    dst[1] = packed[1];
-    if (lane == 0)
+    *reinterpret_cast<uint4 *>(p.out + (size_t)flat * kDv + d0) = packed;
+    if (lane == 0 && d0 == 0)
         p.lse[((size_t)seq * p.h_q + r % p.h_q) * p.s_q + r / p.h_q] =
             m == -INFINITY ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
 }
@@ -675,8 +716,15 @@ size_t shared_smem_bytes() { return sizeof(shr::Smem); }
 cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
                           const CUtensorMap &map_q, cudaStream_t stream) {
     const size_t smem = shared_smem_bytes();
-    cudaError_t e = cudaFuncSetAttribute(shr::shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    static std::atomic<bool> ready[kMaxDevices];  // the kernel's shared-memory limit, raised once per device
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(shr::shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * p.num_parts, 1, 1);
     cfg.blockDim = dim3(shr::kThreads, 1, 1);
@@ -693,7 +741,7 @@ cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const
 }
 
 cudaError_t launch_shared_merge(const SharedParams &p, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((p.total_rows + shr::kMergeWarps - 1) / shr::kMergeWarps);
+    const unsigned grid = (unsigned)((2 * (int64_t)p.total_rows + shr::kMergeWarps - 1) / shr::kMergeWarps);
     shr::merge_kernel<<<grid, 32 * shr::kMergeWarps, 0, stream>>>(p);
     return cudaGetLastError();
 }
