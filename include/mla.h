@@ -352,8 +352,8 @@ int mla_rope_init(mla_rope *rope, double base, int interleaved, double factor, i
  *               i / s_q, at position max(seqlens[i / s_q], 0) + i % s_q (seqlens int32[tokens / s_q]: the
  *               lengths BEFORE the new tokens, as for the appends)
  *   rope        host pointer, read during the call
- * Strides are in elements, non-negative multiples of 8; x and y 16-byte aligned; tokens in [1, 2^24],
- * heads in [1, 4096]. Angles and products in fp32, one rounding to bf16 (nearest even). Asynchronous on
+ * Strides are in elements, non-negative multiples of 8 (x may repeat rows, y's rows must not overlap); x and
+ * y 16-byte aligned; tokens in [1, 2^24], heads in [1, 4096]. Angles and products in fp32, one rounding to bf16 (nearest even). Asynchronous on
  * `stream`; allocates nothing. Errors as for mla_head_gemm.
  */
 int mla_rope_q(const void *x, int64_t ldx, int64_t x_head_stride, void *y, int64_t ldy, int64_t y_head_stride, int tokens,

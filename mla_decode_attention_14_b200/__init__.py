@@ -491,18 +491,18 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, shared_table: torch.T
     if meta.num_splits.get_device() != i:
         raise ValueError("meta must be on cuda:%d" % i)
     if out is None:
-        out = torch.empty((b, s_q, h_q, D_V), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty((b, s_q, h_q, D_V))
     elif not _is(out, torch.bfloat16, i, 4) or out.shape != (b, s_q, h_q, D_V):
         _refuse(out, "out", torch.bfloat16, i, 4)
         raise ValueError("out must be [b, s_q, h_q, 512]")
     if lse is None:
-        lse = torch.empty((b, h_q, s_q), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((b, h_q, s_q), dtype=torch.float32)
     elif not _is(lse, torch.float32, i, 3) or lse.shape != (b, h_q, s_q):
         _refuse(lse, "lse", torch.float32, i, 3)
         raise ValueError("lse must be [b, h_q, s_q]")
     ws_bytes = L.mla_shared_workspace_bytes(b, s_q, h_q, shared_blocks, meta.num_parts)
     if workspace is None:
-        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty((ws_bytes,), dtype=torch.uint8)
     elif workspace.get_device() != i or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError("workspace must be a contiguous tensor of at least %d bytes on cuda:%d" % (ws_bytes, i))

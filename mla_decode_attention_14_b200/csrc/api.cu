@@ -678,6 +678,10 @@ int mla_rope_q(const void *x, int64_t ldx, int64_t x_head_stride, void *y, int64
         y_head_stride < 0 || ldx > kMaxStride || ldy > kMaxStride || x_head_stride > kMaxStride ||
         y_head_stride > kMaxStride)
         return MLA_ERR_INVALID_ARG;
+    // no two rows of y overlap: heads inside a token's row, or tokens inside a head's
+    const int64_t yh = heads > 1 ? y_head_stride : 64, yt = tokens > 1 ? ldy : 64;
+    if (yh < 64 || yt < 64 || (heads > 1 && tokens > 1 && yt < (heads - 1) * yh + 64 && yh < (tokens - 1) * yt + 64))
+        return MLA_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(y, 16) || !aligned(positions, 4) || !aligned(seqlens, 4)) return MLA_ERR_INVALID_ARG;
     int rc = check_device();
     if (rc != MLA_OK) return rc;

@@ -96,6 +96,10 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
         : "memory");
 }
+// Programmatic dependent launch: the kernel may have been put on the GPU before the one ahead of it in the
+// stream has ended; here that one has, and its writes are visible.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Brings a box into L2 only.
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"

@@ -587,6 +587,7 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         prefetch_tensormap(&map_v);
         prefetch_tensormap(&map_q);
     }
+    wait_for_previous_kernel();  // the set-up above needs nothing of it
     Walker w;
     w.init(meta, p);
     tc_fence_before();
@@ -633,6 +634,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_kernel(const Shared
     const int d0 = (int)(w & 1) * (kDv / 2) + 8 * lane;
     const int seq = flat / p.rows, r = flat % p.rows;
     const int ou = p.prefix_units + seq * p.groups + r / 128;
+    wait_for_previous_kernel();
     const int o0 = p.num_splits[ou], no = p.num_splits[ou + 1] - o0;
     int p0 = 0, np = 0, ob = 0;
     if (p.prefix_units > 0) {
@@ -713,6 +715,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_kernel(const Shared
 
 size_t shared_smem_bytes() { return sizeof(shr::Smem); }
 
+// Both kernels take programmatic launches, without an early trigger: their launch overlaps the end of the
+// kernel before them (a small call back to back 17.3 -> 13.7 us; triggering early was slower).
 cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
                           const CUtensorMap &map_q, cudaStream_t stream) {
     const size_t smem = shared_smem_bytes();
@@ -730,20 +734,29 @@ cudaError_t launch_shared(const SharedParams &p, const CUtensorMap &map_k, const
     cfg.blockDim = dim3(shr::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, shr::shared_kernel, map_k, map_v, map_q, p);
 }
 
 cudaError_t launch_shared_merge(const SharedParams &p, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((2 * (int64_t)p.total_rows + shr::kMergeWarps - 1) / shr::kMergeWarps);
-    shr::merge_kernel<<<grid, 32 * shr::kMergeWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((2 * (int64_t)p.total_rows + shr::kMergeWarps - 1) / shr::kMergeWarps), 1, 1);
+    cfg.blockDim = dim3(32 * shr::kMergeWarps, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, shr::merge_kernel, p);
 }
 
 }  // namespace mla
