@@ -697,7 +697,6 @@ int mla_rope_q(const void *x, int64_t ldx, int64_t x_head_stride, void *y, int64
     p.tokens = tokens;
     p.heads = heads;
     p.s_q = positions ? 1 : s_q;
-    p.chunks = 0;
     cudaError_t e = launch_rope_query(p, *rope, static_cast<cudaStream_t>(stream));
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(e);

@@ -12,7 +12,7 @@ struct QueryParams {
     __nv_bfloat16 *y;
     int64_t ldx, x_head, ldy, y_head;  // elements
     const int32_t *positions, *seqlens;
-    int tokens, heads, s_q, chunks;    // chunks: warps per token
+    int tokens, heads, s_q;
 };
 
 struct AppendParams {
