@@ -541,8 +541,10 @@ int64_t mla_shared_units(int batch, int s_q, int h_q, int shared_blocks) {
     return shared_shape(batch, s_q, h_q, shared_blocks, &sh) ? sh.units : 0;
 }
 
-// Per-piece start-up cost in 128-token tiles.
-int mla_shared_fixed_cost(void) { return 2; }
+// Per-piece start-up cost in 128-token tiles: a piece spends about five tiles' time on its query, the first K from HBM,
+// the drain of its last tile and its output. Measured (back to back; 2, 4, 5, 6, 8 tiles): 33 x 64 heads over a shared 65536
+// 344, 318, 307, 316, 315 us; 64 x 16 heads 55.0, 55.5, 56.3, 56.4, 57.6; 128 x 128 heads 184, 183, 182, 183, 184.
+int mla_shared_fixed_cost(void) { return 5; }
 
 size_t mla_shared_workspace_bytes(int batch, int s_q, int h_q, int shared_blocks, int num_parts) {
     SharedShape sh;

@@ -589,11 +589,13 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     }
     wait_for_previous_kernel();  // the set-up above needs nothing of it
     Walker w;
-    w.init(meta, p);
+    const bool early = warp == 0 || warp == 3;  // the loads are waited for: their first piece during the set-up
+    if (early) w.init(meta, p);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist
     tc_fence_after();
+    if (!early) w.init(meta, p);
     const uint32_t tmem = sm.tmem_base;
 
     if (warp == 0) {
