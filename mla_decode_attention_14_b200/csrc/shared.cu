@@ -180,6 +180,8 @@ struct Loader {
     const SharedParams &p;
     const CUtensorMap *map_k, *map_v, *map_q;
     uint32_t rank;
+    // K of own blocks and Q leave L2 first; V is hinted like shared keys, since its two halves are read by both
+    // CTAs and right after K (evicting it first cost 1-2%: 306 against 302 us of a 65,536-token prefix)
     uint64_t pol_shared, pol_own;
     int k_fills, v_fills, tails;  // groups and blocks issued; partial tiles among them
 
@@ -209,7 +211,7 @@ struct Loader {
             const int y = *(volatile int *)&sm.row[g % kAhead][t];
             if (!tail) {
                 if (rank == 0) mbar_arrive_expect_tx(&sm.v_full[t], 2 * kValueBytes);
-                tma_load_3d_pair(sm.v[t], map_v, 0, y, 4 * (int)rank, map_to_rank(&sm.v_full[t], 0), pol_own);
+                tma_load_3d_pair(sm.v[t], map_v, 0, y, 4 * (int)rank, map_to_rank(&sm.v_full[t], 0), pol_shared);
             } else {
                 if (rank == 0) mbar_arrive(&sm.v_full[t]);  // keeps the phases in step
                 if (t == 0) mbar_arrive_expect_tx(&sm.tail_full, 2 * kValueBytes);
@@ -627,8 +629,9 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 // ---------------------------------------------------------------- merging the pieces of a row
 // Two warps per row, 8 dims per lane: the pieces of its prefix unit, then those of its own unit. Bound by
 // latency (a few dependent rounds of loads) and, for many rows, by the partials' bytes (2 KB a piece and
-// row, from L2): lane k reads the lse of piece k, four pieces' outputs are in flight per warp beside it.
-constexpr int kMergeWarps = 8, kMergeFly = 4;
+// row, from L2): lane k reads the lse of piece k, two pieces' outputs are in flight per warp beside it. Most
+// rows have two or three pieces: four in flight load some twice, and cost 1.5 of 180 us at 16,384 rows.
+constexpr int kMergeWarps = 8, kMergeFly = 2;
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_kernel(const SharedParams p) {
     const int64_t w = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     const int flat = (int)(w >> 1), lane = threadIdx.x & 31;
