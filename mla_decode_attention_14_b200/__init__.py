@@ -186,6 +186,8 @@ class Metadata:
 class SharedMetadata(Metadata):
     """Schedule of :func:`decode_shared`, produced by :func:`get_metadata_shared`."""
     shared_blocks: int = 0
+    batch: int = 0            # 0: unknown (a schedule put together by hand), as is the next
+    workspace_bytes: int = 0  # what decode_shared needs, asked once
 
 
 def default_num_parts(h_q: int, s_q: int, device=None) -> int:
@@ -432,6 +434,14 @@ def _launch(name: str, index: int, stream, *args):
         raise MLAError(name, rc)
 
 
+def _new(like, stream, shape, dtype):
+    """An empty tensor for a call on ``stream``: of that stream's memory, which nothing else in flight uses."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def get_metadata_shared(seqlens: torch.Tensor, h_q: int, s_q: int, shared_blocks: int, num_parts: int | None = None,
                         fixed_cost: int | None = None, stream=None) -> SharedMetadata:
     """Schedule for :func:`decode_shared` (``mla_get_metadata_shared``): ``seqlens`` int32 ``[b]`` are whole
@@ -445,11 +455,12 @@ def get_metadata_shared(seqlens: torch.Tensor, h_q: int, s_q: int, shared_blocks
     units = lib().mla_shared_units(b, s_q, h_q, shared_blocks)
     if units < 1:
         raise MLAError("mla_shared_units", 1)
-    tm = torch.empty((num_parts, META_INTS), dtype=torch.int32, device=dev)
-    ns = torch.empty((units + 1,), dtype=torch.int32, device=dev)
+    tm = _new(seqlens, stream, (num_parts, META_INTS), torch.int32)
+    ns = _new(seqlens, stream, (units + 1,), torch.int32)
     _launch("mla_get_metadata_shared", dev.index, stream, seqlens.data_ptr(), b, s_q, h_q, shared_blocks, num_parts,
             fixed_cost, tm.data_ptr(), ns.data_ptr())
-    return SharedMetadata(tm, ns, num_parts, fixed_cost, h_q, s_q, 0, shared_blocks)
+    return SharedMetadata(tm, ns, num_parts, fixed_cost, h_q, s_q, 0, shared_blocks, b,
+                          shared_workspace_bytes(b, s_q, h_q, shared_blocks, num_parts))
 
 
 def shared_workspace_bytes(batch: int, s_q: int, h_q: int, shared_blocks: int, num_parts: int) -> int:
@@ -465,7 +476,7 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, shared_table: torch.T
     ``shared_table`` int32 ``[shared_blocks]``: the prefix's blocks; row b of ``block_table`` holds sequence b's
     blocks from entry ``shared_blocks`` on (earlier entries are not read); ``seqlens`` are whole lengths.
     Returns ``(out bf16 [b, s_q, h_q, 512], lse fp32 [b, h_q, s_q])``, as :func:`decode` with tables that
-    all begin with ``shared_table``.
+    all begin with ``shared_table``. Tensors made here belong to ``stream`` (the current one by default).
     """
     i = q.get_device()
     if not (i >= 0 and _is(q, torch.bfloat16, i, 4)):
@@ -484,25 +495,26 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, shared_table: torch.T
         _refuse(seqlens, "seqlens", torch.int32, i, 1)
     if block_table.shape[0] != b or seqlens.shape[0] != b:
         raise ValueError("batch mismatch between q, block_table and seqlens")
-    L, shared_blocks = lib(), shared_table.shape[0]
+    shared_blocks = shared_table.shape[0]
     if not isinstance(meta, SharedMetadata) or meta.h_q != h_q or meta.s_q != s_q or meta.shared_blocks != shared_blocks \
-            or meta.num_splits.shape[0] != L.mla_shared_units(b, s_q, h_q, shared_blocks) + 1:
+            or (meta.batch or b) != b or \
+            (not meta.batch and meta.num_splits.shape[0] != lib().mla_shared_units(b, s_q, h_q, shared_blocks) + 1):
         raise ValueError("metadata was computed for another shape (use get_metadata_shared)")
     if meta.num_splits.get_device() != i:
         raise ValueError("meta must be on cuda:%d" % i)
     if out is None:
-        out = q.new_empty((b, s_q, h_q, D_V))
+        out = _new(q, stream, (b, s_q, h_q, D_V), torch.bfloat16)
     elif not _is(out, torch.bfloat16, i, 4) or out.shape != (b, s_q, h_q, D_V):
         _refuse(out, "out", torch.bfloat16, i, 4)
         raise ValueError("out must be [b, s_q, h_q, 512]")
     if lse is None:
-        lse = q.new_empty((b, h_q, s_q), dtype=torch.float32)
+        lse = _new(q, stream, (b, h_q, s_q), torch.float32)
     elif not _is(lse, torch.float32, i, 3) or lse.shape != (b, h_q, s_q):
         _refuse(lse, "lse", torch.float32, i, 3)
         raise ValueError("lse must be [b, h_q, s_q]")
-    ws_bytes = L.mla_shared_workspace_bytes(b, s_q, h_q, shared_blocks, meta.num_parts)
+    ws_bytes = meta.workspace_bytes or shared_workspace_bytes(b, s_q, h_q, shared_blocks, meta.num_parts)
     if workspace is None:
-        workspace = q.new_empty((ws_bytes,), dtype=torch.uint8)
+        workspace = _new(q, stream, (ws_bytes,), torch.uint8)
     elif workspace.get_device() != i or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError("workspace must be a contiguous tensor of at least %d bytes on cuda:%d" % (ws_bytes, i))
@@ -636,7 +648,9 @@ def _append_rope(fp8, new_kv, kv_cache, block_table, seqlens, kv_scale, rope, no
             _refuse(cu_new, "cu_new", torch.int32, i, 1)
         if cu_new.shape[0] != b + 1:
             raise ValueError("cu_new must hold b + 1 values")
-        tokens, n_new, cu, ld = xs[0], 0, cu_new.data_ptr(), st[0] if xs[0] > 1 else 0
+        tokens, n_new, cu, ld = xs[0], 0, cu_new.data_ptr(), st[0]
+    if tokens > 1 and ld < D_QK:
+        raise ValueError("new_kv must not repeat or overlap its rows (its tokens are %d elements apart)" % ld)
     weight = at = None
     if norm_weight is not None:
         if not _is(norm_weight, torch.bfloat16, i, 1) or norm_weight.shape[0] != D_V:
@@ -651,7 +665,7 @@ def _append_rope(fp8, new_kv, kv_cache, block_table, seqlens, kv_scale, rope, no
         at = positions.data_ptr()
     if tokens == 0:
         return
-    head = (new_kv.data_ptr(), ld or D_QK, tokens, n_new, cu, weight, eps, rope.ref, at, kv_cache.data_ptr(), kv_shape[0])
+    head = (new_kv.data_ptr(), ld if tokens > 1 else D_QK, tokens, n_new, cu, weight, eps, rope.ref, at, kv_cache.data_ptr(), kv_shape[0])
     tail = (block_table.data_ptr(), block_table.shape[1], seqlens.data_ptr(), b)
     if fp8:
         _launch("mla_append_kv_rope_fp8", i, stream, *head, kv_scale, *tail)

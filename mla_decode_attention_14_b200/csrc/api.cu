@@ -628,9 +628,9 @@ int mla_decode_shared(const void *q, const void *kv_cache, int64_t num_blocks, c
     p.num_parts = num_parts;
     p.causal = causal;
     p.out_v8 = aligned(out, 32);
-    // a masked score is -inf, and -inf * 0 is no number: scale 0 (uniform weights) becomes a scale that no
-    // finite score can tell from it
-    p.scale_log2 = std::fmax(scale * 1.4426950408889634f, 1e-37f);
+    // a masked score is -inf, and -inf * 0 is no number: scale 0 (uniform weights) becomes a (subnormal) scale
+    // that moves even the largest finite score, 2^128, by less than 2^-18
+    p.scale_log2 = std::fmax(scale * 1.4426950408889634f, 0x1p-146f);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_shared(p, map_k, map_v, map_q, st);
     g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -644,7 +644,7 @@ int mla_rope_init(mla_rope *rope, double base, int interleaved, double factor, i
                   double beta_slow, double magnitude) {
     if (!rope || !(base > 1.0) || !std::isfinite(base) || (interleaved != 0 && interleaved != 1) || !(factor >= 1.0) ||
         !std::isfinite(factor) || original_len < 0 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
-        !std::isfinite(beta_fast) || !std::isfinite(magnitude))
+        !std::isfinite(beta_fast) || !std::isfinite((float)magnitude))
         return MLA_ERR_INVALID_ARG;
     constexpr int dim = MLA_D_QK - MLA_D_V;
     const double pi = 3.14159265358979323846;

@@ -107,7 +107,7 @@ def test_rope_frequencies(kw):
 
 @pytest.mark.parametrize("bad", [dict(base=1.0), dict(base=float("inf")), dict(base=float("nan")), dict(factor=0.5),
                                  dict(factor=float("nan")), dict(original_len=-1), dict(beta_slow=0.0),
-                                 dict(beta_fast=0.5), dict(magnitude=float("nan"))])
+                                 dict(beta_fast=0.5), dict(magnitude=float("nan")), dict(magnitude=1e39)])
 def test_rope_refuses(bad):
     with pytest.raises(mla.MLAError):
         mla.rope(**bad)

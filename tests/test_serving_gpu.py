@@ -123,6 +123,8 @@ def test_metadata_of_another_kind_is_refused():
         mla.decode(q, kv, bt, sl, 0.1, False, shared)
     with pytest.raises(ValueError):
         mla.decode_shared(q, kv, table[:0], bt, sl, 0.1, False, shared)
+    with pytest.raises(ValueError):
+        mla.decode_shared(q[:1], kv, table, bt[:1], sl[:1], 0.1, False, shared)
     for bad in (dict(out=torch.empty((2, 1, 128, 512), device="cuda")), dict(workspace=torch.empty(8, device="cuda")),
                 dict(lse=torch.empty((2, 1, 128), device="cuda"))):
         with pytest.raises((ValueError, TypeError)):
@@ -197,6 +199,44 @@ def test_streams_workspaces_and_repeats():
     assert mla.check_status() == 0
     for out, lse in got:
         assert torch.equal(out, o0) and torch.equal(lse, l0)
+
+
+def test_tensors_made_by_a_call_belong_to_its_stream():
+    """Another stream fills whatever memory is free while the calls run: nothing of theirs is."""
+    inp = make(24, 16, 1, 40, [2561 + 40 * i for i in range(24)], seed=31)
+    q, kv, table, bt, sl = device_inputs(inp)
+    meta = mla.get_metadata_shared(sl, 16, 1, 40)
+    o0, l0 = mla.decode_shared(q, kv, table, bt, sl, W.SCALE, False, meta)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        m = mla.get_metadata_shared(sl, 16, 1, 40, stream=s)
+        got.append(mla.decode_shared(q, kv, table, bt, sl, W.SCALE, False, m, stream=s) + (m,))
+        for size in (m.workspace_bytes, 2 * o0.numel(), 4 * l0.numel()):
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert mla.check_status() == 0
+    for out, lse, m in got:
+        assert torch.equal(m.tile_meta, meta.tile_meta) and torch.equal(out, o0) and torch.equal(lse, l0)
+
+
+def test_repeated_rows_are_refused_by_the_appends():
+    """A token broadcast over the batch has rows 0 elements apart: refused, not read as if they were 576 apart."""
+    kv = torch.zeros((4, 64, 1, 576), dtype=torch.bfloat16, device="cuda")
+    kv8 = torch.zeros((4, 64, 1, 640), dtype=torch.uint8, device="cuda")
+    bt, sl = torch.arange(3, dtype=torch.int32, device="cuda")[:, None].contiguous(), torch.zeros(3, dtype=torch.int32, device="cuda")
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    row, r = torch.ones((1, 1, 576), dtype=torch.bfloat16, device="cuda"), mla.rope()
+    for x, c in ((row.expand(3, 1, 576), None), (row[0].expand(3, 576), cu), (row.expand(3, 2, 576), None)):
+        with pytest.raises(ValueError):
+            mla.append_kv_rope(x, kv, bt, sl, r, cu_new=c)
+        with pytest.raises(ValueError):
+            mla.append_kv_rope_fp8(x, kv8, bt, sl, 0.5, r, cu_new=c)
+    torch.cuda.synchronize()
+    assert not kv.any() and not kv8.any()
+    mla.append_kv_rope(row, kv, bt[:1], sl[:1], r)  # one token has no distance to the next
+    assert torch.equal(kv[0, 0, 0, :512], row[0, 0, :512])
 
 
 def test_output_on_a_16_byte_boundary():

@@ -127,6 +127,17 @@ def test_scales(scale):
     check(*run(inp, scale=scale, num_parts=2), reference(inp, scale, False))
 
 
+def test_scale_zero_of_huge_scores():
+    """Scores of up to +-2^123 keep uniform weights."""
+    inp = make(2, 16, 1, 2, [150, 200], seed=6)
+    q, kv = W.bf16_bits_to_f32(inp["q"]), W.bf16_bits_to_f32(inp["kv"])
+    q[..., 575] = 2.0 ** 62
+    live = np.isfinite(kv[..., 575])
+    kv[..., 575] = np.where(live, np.where(kv[..., 575] > 0, 2.0 ** 61, -2.0 ** 61), kv[..., 575])
+    inp["q"], inp["kv"] = W.f32_to_bf16_bits(q), W.f32_to_bf16_bits(kv)
+    check(*run(inp, scale=0.0, num_parts=2), reference(inp, 0.0, False))
+
+
 def test_growing_scores_rescale():
     """Keys whose scores grow along the sequence: the running maximum moves in every tile."""
     inp = make(2, 128, 1, 4, [700, 640], seed=5, nan_tails=False)
