@@ -97,7 +97,8 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 // Programmatic dependent launch: the kernel may have been put on the GPU before the one ahead of it in the
-// stream has ended; here that one has, and its writes are visible.
+// stream has ended; here that one has, and its writes are visible. (Such kernels read by plain loads, not
+// __ldg: what they read is not constant for as long as they run, only from here on.)
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Brings a box into L2 only.

@@ -10,6 +10,7 @@
 // error of at most 2^-26 turns), sine and cosine are taken there, and each result is rounded to bf16 once.
 #include <cuda_fp8.h>
 
+#include "pair_ptx.cuh"
 #include "rope.cuh"
 
 namespace mla {
@@ -17,7 +18,7 @@ namespace rp {
 
 constexpr int kRopeDims = kDqk - kDv;      // 64
 constexpr int kPairs = kRopeDims / 2;      // one per lane
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;                   // per block
 constexpr int kF8Record = MLA_FP8_RECORD_BYTES;
 
 // cos and sin (times the magnitude) of pair `lane` at position `pos`
@@ -39,11 +40,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // Query rows: bounded by bytes (128 in, 128 out per token and head) for prompts, by latency for a decode
 // step. A warp takes up to 16 heads of one token: its lanes compute the token's 32 rotations once and pass
 // them through shared memory; four lanes then serve a row (8 pairs and 2 x 16 bytes each), so a warp moves
-// 8 rows at a time, both batches' loads issued before the angles are needed.
+// 8 rows at a time, both batches' loads issued before the angles are needed. 16,384 tokens of 16 heads (67 MB),
+// cold: 14.0 us, 4.8 TB/s; with a plain launch 16.4.
 constexpr int kRowsPerWarp = 16;
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps) query_kernel(const QueryParams p, const __grid_constant__ mla_rope rope) {
     __shared__ float2 cs[kWarps][kPairs];
+    sm100::wait_for_previous_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tok = blockIdx.x * kWarps + warp;
     if (tok >= p.tokens) return;
@@ -93,14 +96,14 @@ __global__ void __launch_bounds__(32 * kWarps) query_kernel(const QueryParams p,
 // The sequence b that packed row i belongs to and cu[b] (the last b with cu[b] <= i; empty sequences are stepped
 // over), by a 32-way search of the whole warp; (-1, 0) for a row of no sequence. In a broken `cu` b is
 // still a sequence.
-__device__ __forceinline__ int2 find_sequence(const int32_t *__restrict__ cu, int batch, int i, int lane) {
-    const int end = __ldg(&cu[batch]);
+__device__ __forceinline__ int2 find_sequence(const int32_t *cu, int batch, int i, int lane) {
+    const int end = cu[batch];
     int lo = 0, n = batch, start = 0;  // the answer is in [lo, lo + n); start = cu[lo]
     bool first = true;
     while (n > 1 || first) {
         const int step = (n + 31) >> 5;
         const int at = min(lane * step, n - 1);
-        const int c = __ldg(&cu[lo + at]);
+        const int c = cu[lo + at];
         const uint32_t below = __ballot_sync(0xffffffffu, c <= i && lane * step < n);
         if (first && !(below & 1u)) return make_int2(-1, 0);  // before the first sequence
         const int k = 31 - __clz(below | 1u);
@@ -115,19 +118,22 @@ __device__ __forceinline__ int2 find_sequence(const int32_t *__restrict__ cu, in
 // New tokens into the cache: bounded by bytes (1152 in, 1152 or 640 out per token) for prompts, by
 // latency for a decode step. One warp per token: a lane holds two 16-byte chunks of the latent and one rotary
 // pair; the sum of squares is a warp reduction in fp32, and the row is read and written once.
-// (8 blocks an SM: 21.7 us for 36,800 packed tokens of a bf16 cache, cold, against 22.3 with the registers of 6;
-// two or four tokens a warp with all loads ahead: 25 and 30 us.)
+// The input is dead once read, and a prompt's rows are not read back before much else has been: loads and latent
+// stores are hinted evict-first. 36,800 packed tokens into a bf16 cache, cold: 18.6 us (4.5 TB/s); blocks of 8 and 16
+// warps 18.9 and 20.0, without the hints 19.5, with a plain launch 20.5; the registers of 48 instead of 64 warps
+// an SM cost 0.6 us, two or four tokens a warp with all loads ahead 4 and 9 (no writes beside the reads).
 template <bool F8, bool INTERLEAVED>
-__global__ void __launch_bounds__(32 * kWarps, 8) append_kernel(const AppendParams p, const __grid_constant__ mla_rope rope) {
+__global__ void __launch_bounds__(32 * kWarps, 16) append_kernel(const AppendParams p, const __grid_constant__ mla_rope rope) {
+    sm100::wait_for_previous_kernel();
     const int lane = threadIdx.x & 31;
     const int w = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (w >= p.tokens) return;
     const __nv_bfloat16 *src = p.x + (int64_t)w * p.ld;
     const uint4 *chunks = reinterpret_cast<const uint4 *>(src);
-    const uint4 xa = __ldg(chunks + lane), xb = __ldg(chunks + 32 + lane);
+    const uint4 xa = __ldcs(chunks + lane), xb = __ldcs(chunks + 32 + lane);
     // the rotary pair: one word (interleaved); half layout: the values of dims 2 (lane % 16), + 1 of this lane's half,
     // so that the row is read in whole words; the pair's other value comes from lane ^ 16
-    const uint32_t two = __ldg(reinterpret_cast<const uint32_t *>(src + kDv) + lane);
+    const uint32_t two = reinterpret_cast<const uint32_t *>(src + kDv)[lane];
     int b, t;  // sequence, place among its new tokens
     if (p.cu_new) {
         const int2 f = find_sequence(p.cu_new, p.batch, w, lane);
@@ -138,15 +144,15 @@ __global__ void __launch_bounds__(32 * kWarps, 8) append_kernel(const AppendPara
         b = w / p.n_new;
         t = w - b * p.n_new;
     }
-    const int64_t at = (int64_t)max(__ldg(&p.seqlens[b]), 0) + t;
+    const int64_t at = (int64_t)max(p.seqlens[b], 0) + t;
     const int64_t bi = at / kBlk;
-    const int32_t phys = bi < p.bt_stride ? __ldg(&p.block_table[(size_t)b * p.bt_stride + bi]) : -1;
+    const int32_t phys = bi < p.bt_stride ? p.block_table[(size_t)b * p.bt_stride + bi] : -1;
     if (phys < 0 || (int64_t)phys >= p.num_blocks) {
         if (lane == 0) raise_error(kErrBounds);
         return;
     }
     const int64_t row = (int64_t)phys * kBlk + at % kBlk;
-    const int64_t pos = p.positions ? (int64_t)__ldg(&p.positions[w]) : at;
+    const int64_t pos = p.positions ? (int64_t)p.positions[w] : at;
     uint32_t rotated;
     if constexpr (INTERLEAVED) {
         const float2 cs = turn(rope, pos, lane);
@@ -170,8 +176,8 @@ __global__ void __launch_bounds__(32 * kWarps, 8) append_kernel(const AppendPara
         v[2 * i + 1] = hi_f(xw[i]);
     }
     if (p.weight) {
-        const uint4 wa = __ldg(reinterpret_cast<const uint4 *>(p.weight) + lane),
-                    wb = __ldg(reinterpret_cast<const uint4 *>(p.weight) + 32 + lane);
+        const uint4 wa = reinterpret_cast<const uint4 *>(p.weight)[lane],
+                    wb = reinterpret_cast<const uint4 *>(p.weight)[32 + lane];
         const uint32_t ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
         float ss = 0.f;
 #pragma unroll
@@ -202,29 +208,39 @@ __global__ void __launch_bounds__(32 * kWarps, 8) append_kernel(const AppendPara
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        reinterpret_cast<uint4 *>(dst)[lane] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint4 *>(dst)[32 + lane] = make_uint4(o[4], o[5], o[6], o[7]);
+        __stcs(reinterpret_cast<uint4 *>(dst) + lane, make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(reinterpret_cast<uint4 *>(dst) + 32 + lane, make_uint4(o[4], o[5], o[6], o[7]));
     }
     reinterpret_cast<uint32_t *>(dst + (F8 ? kDv : kDv * 2))[lane] = rotated;
+}
+
+// A programmatic launch: it overlaps the end of the kernel before it, whose results every thread awaits first.
+template <class P>
+cudaError_t launch(void (*kernel)(P, mla_rope), dim3 grid, const P &p, const mla_rope &rope, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(32 * kWarps, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, rope);
 }
 
 }  // namespace rp
 
 cudaError_t launch_rope_query(const rp::QueryParams &p, const mla_rope &rope, cudaStream_t stream) {
     const dim3 grid((p.tokens + rp::kWarps - 1) / rp::kWarps, (p.heads + rp::kRowsPerWarp - 1) / rp::kRowsPerWarp);
-    if (rope.interleaved)
-        rp::query_kernel<true><<<grid, 32 * rp::kWarps, 0, stream>>>(p, rope);
-    else
-        rp::query_kernel<false><<<grid, 32 * rp::kWarps, 0, stream>>>(p, rope);
-    return cudaGetLastError();
+    return rp::launch(rope.interleaved ? rp::query_kernel<true> : rp::query_kernel<false>, grid, p, rope, stream);
 }
 
 cudaError_t launch_append_rope(const rp::AppendParams &p, const mla_rope &rope, bool fp8, cudaStream_t stream) {
     const unsigned grid = (unsigned)((p.tokens + rp::kWarps - 1) / rp::kWarps);
     auto kernel = fp8 ? (rope.interleaved ? rp::append_kernel<true, true> : rp::append_kernel<true, false>)
                       : (rope.interleaved ? rp::append_kernel<false, true> : rp::append_kernel<false, false>);
-    kernel<<<grid, 32 * rp::kWarps, 0, stream>>>(p, rope);
-    return cudaGetLastError();
+    return rp::launch(kernel, dim3(grid), p, rope, stream);
 }
 
 }  // namespace mla

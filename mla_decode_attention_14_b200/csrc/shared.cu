@@ -107,7 +107,7 @@ struct Walker {
                 pc.seq = o / p.groups;
                 pc.group = o % p.groups;
                 pc.first_blk = p.prefix_units > 0 ? p.shared_blocks : 0;
-                pc.end_tok = clamp_len(__ldg(&p.seqlens[pc.seq]));
+                pc.end_tok = clamp_len(p.seqlens[pc.seq]);
             }
             pc.end_blk = num_blocks_of(pc.end_tok);
             const int w = (max(pc.end_blk - pc.first_blk, 0) + 1) / 2;
@@ -115,8 +115,8 @@ struct Walker {
             pc.hi = u == end_unit ? min(end_tile, w) : w;
             if (pc.hi <= pc.lo) continue;
             // partial slots: the prefix units' of 128 rows, then the own units' of own_rows
-            const int s0 = __ldg(&p.num_splits[u]), own0 = __ldg(&p.num_splits[p.prefix_units]);
-            pc.nsplit = __ldg(&p.num_splits[u + 1]) - s0;
+            const int s0 = p.num_splits[u], own0 = p.num_splits[p.prefix_units];
+            pc.nsplit = p.num_splits[u + 1] - s0;
             const int slot = s0 + (u == begin_unit ? first_piece : 0) - (pc.seq < 0 ? 0 : own0);
             const int slots = (pc.seq < 0 ? p.prefix_units : p.units - p.prefix_units) + p.num_parts;
             if (pc.nsplit < 1 || slot < 0 || slot >= slots) continue;  // malformed
@@ -163,9 +163,9 @@ __device__ __forceinline__ int block_row(const SharedParams &p, const Piece &pc,
     if (blk >= pc.end_blk) return none;
     int phys;
     if (blk < p.shared_blocks)
-        phys = __ldg(&p.shared_table[blk]);
+        phys = p.shared_table[blk];
     else
-        phys = blk < p.bt_stride ? __ldg(&p.block_table[(size_t)pc.seq * p.bt_stride + blk]) : -1;
+        phys = blk < p.bt_stride ? p.block_table[(size_t)pc.seq * p.bt_stride + blk] : -1;
     if (phys < 0 || (int64_t)phys >= p.num_blocks) {
         bad = true;
         return none;
@@ -413,7 +413,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
             const int seq = w.pc.seq < 0 ? min(flat, p.total_rows - 1) / p.rows : w.pc.seq;
             const int r = flat - seq * p.rows;
             row_ok = w.pc.seq < 0 ? flat < p.total_rows : r < p.rows;
-            vis = row_ok ? visible_keys(__ldg(&p.seqlens[seq]), p.s_q, r / p.h_q, p.causal) : 0;
+            vis = row_ok ? visible_keys(p.seqlens[seq], p.s_q, r / p.h_q, p.causal) : 0;
             vis = min(vis, min(w.pc.first_blk + 2 * w.pc.hi, w.pc.end_blk) * kBlk);
         }
         const int key0 = w.blk() * kBlk + blk * kBlk + 32 * th;
