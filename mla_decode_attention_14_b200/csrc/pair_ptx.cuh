@@ -18,7 +18,7 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Bounded waits without a suspend-time hint, by one lane for its warp: with one, a warp was seen to wake up
+// Bounded waits without a suspend-time hint: with one, a warp was seen to wake up
 // to about a thousand cycles after its phase, which the short dependent steps of a pair kernel cannot hide.
 // Same contract as mbar_wait (false: *abort was set, or the bound passed and *abort is now set).
 __device__ __forceinline__ bool mbar_poll_once(uint64_t *bar, uint32_t parity) {
@@ -42,10 +42,10 @@ __device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volati
         }
     }
 }
-__device__ __forceinline__ bool warp_poll(uint64_t *bar, uint32_t parity, volatile int *abort, int lane) {
-    bool ok = true;
-    if (lane == 0) ok = mbar_poll(bar, parity, abort);
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+// For a whole converged warp: all lanes look at once (by lane 0 with a shuffle, a ready phase took 250 cycles).
+__device__ __forceinline__ bool warp_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (__all_sync(0xffffffffu, mbar_poll_once(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort));
 }
 
 // Arrive on a barrier of either CTA given by its shared::cluster address, in order with this thread's own

@@ -187,13 +187,13 @@ struct Loader {
 
     __device__ bool load_k(const Walker &w, int g) {
         const int blk = w.blk() + (int)rank;
-        if (!mbar_wait(&sm.r_full[g % kAhead], (g / kAhead) & 1, &sm.abort)) return false;
+        if (!mbar_poll(&sm.r_full[g % kAhead], (g / kAhead) & 1, &sm.abort)) return false;
         const int y = *(volatile int *)&sm.row[g % kAhead][rank];
         const uint64_t pol = blk < p.shared_blocks ? pol_shared : pol_own;
         const bool first = w.first();
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            if (g > 0 && !mbar_wait(&sm.k_free[i], (g - 1) & 1, &sm.abort)) return false;
+            if (g > 0 && !mbar_poll(&sm.k_free[i], (g - 1) & 1, &sm.abort)) return false;
             const uint32_t bar = map_to_rank(&sm.k_full[i], 0);
             if (rank == 0) mbar_arrive_expect_tx(&sm.k_full[i], (first ? 4 : 2) * kGroupBytes);
             tma_load_3d_pair(sm.k + i * kGroupBytes, map_k, 0, y, kGroupBoxes * i, bar, pol);
@@ -207,7 +207,7 @@ struct Loader {
         const bool tail = w.tail();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (g > 0 && !mbar_wait(&sm.v_free[t], (g - 1) & 1, &sm.abort)) return false;
+            if (g > 0 && !mbar_poll(&sm.v_free[t], (g - 1) & 1, &sm.abort)) return false;
             const int y = *(volatile int *)&sm.row[g % kAhead][t];
             if (!tail) {
                 if (rank == 0) mbar_arrive_expect_tx(&sm.v_full[t], 2 * kValueBytes);
@@ -294,7 +294,7 @@ __device__ void tail_role(Smem &sm, const SharedParams &p, Walker w) {
     int tails = 0;
     for (; w.live; w.advance(p)) {
         if (!w.tail()) continue;
-        if (!warp_poll(&sm.tail_full, tails & 1, &sm.abort, lane)) break;
+        if (!warp_poll(&sm.tail_full, tails & 1, &sm.abort)) break;
         ++tails;
         const int left = w.pc.end_tok - w.blk() * kBlk;  // tokens of the tile (a missing block is zeros)
         if (left < kBlk) zero_rows(sm.v[0], max(left, 0), lane);
@@ -306,11 +306,15 @@ __device__ void tail_role(Smem &sm, const SharedParams &p, Walker w) {
     }
 }
 
-// ---------------------------------------------------------------- warp 1 of the leader: MMAs
+// ---------------------------------------------------------------- warp 1 of the leader, one thread: MMAs
+// Its own instruction stream bounds the tensor cores: with the whole warp in the role and one lane elected for each
+// group, a wait whose phase was there cost about 280 cycles (a branch, a shuffle), an election 75, a reconvergence
+// 90, some 2,500 in all per tile beside 2,176 of MMAs. One elected thread throughout: 306 -> 285 us of a
+// 65,536-token prefix, 179 -> 165 with 128 x 128 heads.
 struct Issuer {
     Smem &sm;
     uint32_t tmem;
-    int lane, tails;
+    int tails;
 
     // S(g) = Q K^T. The score buffer is free: P of tile g - 2 was awaited before this.
     __device__ bool scores(int g) {
@@ -319,18 +323,15 @@ struct Issuer {
         const uint32_t d = tmem + kTmemS + kTmemSCols * (g & 1);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            if (!warp_poll(&sm.k_full[i], g & 1, &sm.abort, lane)) return false;
+            if (!mbar_poll(&sm.k_full[i], g & 1, &sm.abort)) return false;
             tc_fence_after();
-            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4 * kGroupBoxes; ++k) {
-                    const uint64_t off = (uint64_t)(((i * kGroupBoxes + (k >> 2)) * kBox + (k & 3) * 32) >> 4);
-                    mma_ss_pair(d, qd + off, kd + off, id, i + k > 0 ? 1u : 0u);
-                }
-                mma_commit_pair(&sm.k_free[i]);
-                if (i == kGroups - 1) mma_commit_pair(&sm.s_full[g & 1]);
+            for (int k = 0; k < 4 * kGroupBoxes; ++k) {
+                const uint64_t off = (uint64_t)(((i * kGroupBoxes + (k >> 2)) * kBox + (k & 3) * 32) >> 4);
+                mma_ss_pair(d, qd + off, kd + off, id, i + k > 0 ? 1u : 0u);
             }
-            __syncwarp();
+            mma_commit_pair(&sm.k_free[i]);
+            if (i == kGroups - 1) mma_commit_pair(&sm.s_full[g & 1]);
         }
         return true;
     }
@@ -338,32 +339,29 @@ struct Issuer {
     __device__ bool values(int g, bool first, bool tail) {
         constexpr uint32_t id = idesc_bf16_f32(128, 256, 1);  // MN-major B
         const uint64_t pd = smem_desc(smem_addr(sm.p), 16, 1024, 2), vd = smem_desc(smem_addr(sm.v), kBox, 1024, 2);
-        if (!warp_poll(&sm.p_full, g & 1, &sm.abort, lane)) return false;
-        if (tail && !warp_poll(&sm.tail_ready, tails & 1, &sm.abort, lane)) return false;
+        if (!mbar_poll(&sm.p_full, g & 1, &sm.abort)) return false;
+        if (tail && !mbar_poll(&sm.tail_ready, tails & 1, &sm.abort)) return false;
         tails += tail;
         const uint32_t acc0 = first ? 0u : 1u;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (!tail && !warp_poll(&sm.v_full[t], g & 1, &sm.abort, lane)) return false;
+            if (!tail && !mbar_poll(&sm.v_full[t], g & 1, &sm.abort)) return false;
             tc_fence_after();
-            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)  // 16 tokens each
+            for (int k = 0; k < 4; ++k)  // 16 tokens each
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)  // 128 value dims of each CTA
-                        mma_ss_pair(tmem + kTmemO + 128 * n, pd + (uint64_t)((t * kBox + k * 32) >> 4),
-                                    vd + (uint64_t)((t * kValueBytes + 2 * n * kBox + k * 2048) >> 4), id,
-                                    t + k > 0 ? 1u : acc0);
-                mma_commit_pair(&sm.v_free[t]);
-            }
-            __syncwarp();
+                for (int n = 0; n < 2; ++n)  // 128 value dims of each CTA
+                    mma_ss_pair(tmem + kTmemO + 128 * n, pd + (uint64_t)((t * kBox + k * 32) >> 4),
+                                vd + (uint64_t)((t * kValueBytes + 2 * n * kBox + k * 2048) >> 4), id,
+                                t + k > 0 ? 1u : acc0);
+            mma_commit_pair(&sm.v_free[t]);
         }
         return true;
     }
 };
 
 __device__ void mma_role(Smem &sm, const SharedParams &p, Walker w, uint32_t tmem) {
-    Issuer is{sm, tmem, (int)(threadIdx.x & 31), 0};
+    Issuer is{sm, tmem, 0};
     bool first = false, tail = false;  // of the tile before
     for (int g = 0;; ++g) {
         if (w.live && !is.scores(g)) break;
@@ -375,15 +373,12 @@ __device__ void mma_role(Smem &sm, const SharedParams &p, Walker w, uint32_t tme
     }
 }
 
-// Every MMA this warp issued completes before teardown (bounded; independent of the abort flag).
+// Every MMA this thread issued completes before teardown (bounded; independent of the abort flag).
 __device__ void drain_mmas(Smem &sm) {
-    if (elect_one()) {
-        mma_commit_pair_local(&sm.mma_done);
-        const long long t0 = clock64();
-        while (!mbar_sleep_test(&sm.mma_done, 0) && clock64() - t0 < kSpinCycles) {
-        }
+    mma_commit_pair_local(&sm.mma_done);
+    const long long t0 = clock64();
+    while (!mbar_sleep_test(&sm.mma_done, 0) && clock64() - t0 < kSpinCycles) {
     }
-    __syncwarp();
 }
 
 // ---------------------------------------------------------------- warps 4-11: softmax and epilogue
@@ -401,7 +396,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
     // After a failed wait the warp walks on without waiting, so that no named barrier misses it.
     bool dead = false;
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!dead && !warp_poll(bar, parity, &sm.abort, lane)) dead = true;
+        if (!dead && !warp_poll(bar, parity, &sm.abort)) dead = true;
     };
     float m_ref = -INFINITY, l = 0.f;
     int vis = 0, flat = 0;
@@ -557,7 +552,7 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of it is used: no room to align by hand
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const uint32_t rank = cluster_ctarank();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const int32_t *meta = p.tile_meta + (size_t)(blockIdx.x >> 1) * kMetaInts;
     if (smem_addr(smem_raw) & 1023) {  // the swizzled boxes need it; both CTAs of the pair see the same
         if (threadIdx.x == 0) raise_error(kErrBounds);
@@ -601,16 +596,16 @@ shared_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const uint32_t tmem = sm.tmem_base;
 
     if (warp == 0) {
-        if (lane == 0) load_role(sm, p, &map_k, &map_v, &map_q, w, rank);
+        if (elect_one()) load_role(sm, p, &map_k, &map_v, &map_q, w, rank);
     } else if (warp == 1) {
-        if (rank == 0) {
+        if (rank == 0 && elect_one()) {
             mma_role(sm, p, w, tmem);
             drain_mmas(sm);
         }
     } else if (warp == 2) {
         tail_role(sm, p, w);
     } else if (warp == 3) {
-        if (lane == 0) resolve_role(sm, p, &map_k, &map_q, w, rank);
+        if (elect_one()) resolve_role(sm, p, &map_k, &map_q, w, rank);
     } else {
         softmax_role(sm, p, w, tmem, rank);
     }
