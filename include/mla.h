@@ -35,8 +35,10 @@
  * attends each query token to a list of cache positions (top-k) instead of its whole
  * sequence; mla_append_kv / mla_append_kv_fp8 write new tokens into the cache;
  * mla_head_gemm computes the per-head projections on either side (the absorbed q_nope W_UK
- * and o_latent W_UV); mla_decode_host and mla_decode_noalloc are conveniences over
- * mla_decode.
+ * and o_latent W_UV); mla_decode_shared decodes a batch whose sequences share a cached
+ * prefix; mla_rope_q and mla_append_kv_rope / mla_append_kv_rope_fp8 put the rotary positions
+ * on queries and on new tokens (with the latent's RMS norm) on their way into the cache;
+ * mla_decode_host and mla_decode_noalloc are conveniences over mla_decode.
  *
  * Conventions for every call:
  *   - Pointers are DEVICE pointers unless the name says host. All device buffers are
@@ -333,7 +335,7 @@ int mla_decode_shared(const void *q, const void *kv_cache, int64_t num_blocks, c
  *   turns[i] = round(2^64 * f_i / (2 pi)): the angle of position p is the fraction p * turns[i] mod 2^64 of
  *   a full turn, so every int32 position is reduced exactly.
  * Returns MLA_ERR_INVALID_ARG unless base > 1, factor >= 1, original_len >= 0, beta_fast >= beta_slow > 0
- * and all are finite.
+ * and all are finite (magnitude in fp32).
  */
 typedef struct mla_rope {
     uint64_t turns[32];
@@ -353,8 +355,8 @@ int mla_rope_init(mla_rope *rope, double base, int interleaved, double factor, i
  *               lengths BEFORE the new tokens, as for the appends)
  *   rope        host pointer, read during the call
  * Strides are in elements, non-negative multiples of 8 (x may repeat rows, y's rows must not overlap); x and
- * y 16-byte aligned; tokens in [1, 2^24], heads in [1, 4096]. Angles and products in fp32, one rounding to bf16 (nearest even). Asynchronous on
- * `stream`; allocates nothing. Errors as for mla_head_gemm.
+ * y 16-byte aligned; tokens in [1, 2^24], heads in [1, 4096]. Angles and products in fp32, one rounding to
+ * bf16 (nearest even). Asynchronous on `stream`; allocates nothing. Errors as for mla_head_gemm.
  */
 int mla_rope_q(const void *x, int64_t ldx, int64_t x_head_stride, void *y, int64_t ldy, int64_t y_head_stride, int tokens,
                int heads, const int32_t *positions, const int32_t *seqlens, int s_q, const mla_rope *rope,

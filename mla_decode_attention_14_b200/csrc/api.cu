@@ -543,7 +543,7 @@ int64_t mla_shared_units(int batch, int s_q, int h_q, int shared_blocks) {
 
 // Per-piece start-up cost in 128-token tiles: a piece spends about five tiles' time on its query, the first K from HBM,
 // the drain of its last tile and its output. Measured (back to back; 2, 4, 5, 6, 8 tiles): 33 x 64 heads over a shared 65536
-// 344, 318, 307, 316, 315 us; 64 x 16 heads 55.0, 55.5, 56.3, 56.4, 57.6; 128 x 128 heads 184, 183, 182, 183, 184.
+// 311, 281, 271, 278, 278 us; 64 x 16 heads 47.6, 47.2, 48.1, 48.2, 49.6; 128 x 128 heads 160, 161, 158, 159, 161.
 int mla_shared_fixed_cost(void) { return 5; }
 
 size_t mla_shared_workspace_bytes(int batch, int s_q, int h_q, int shared_blocks, int num_parts) {

@@ -24,15 +24,18 @@
 //    ever crosses between the SMs.
 //  * A tile is two cache blocks. S = Q K^T: 36 MMAs of 128 x 128 x 16 (K-major boxes of 64 tokens x 64 dims);
 //    CTA h provides the tokens of block h, all 576 dims of it. O += P V: 16 MMAs of 128 x 256 x 16 (MN-major
-//    boxes); CTA h provides value dims [256h, 256h + 256) of both blocks. The two operands overlap only in
-//    part, and V is loaded on its own (from L2, where K has just put it), so that K's boxes are free as soon
-//    as Gemm1 has read them: K (9 boxes), V (8) and Q (9) have one buffer each, refilled in groups behind the
-//    MMAs, and every load has about a tile's time to land. (Keeping K for Gemm2 moves a quarter less into
-//    shared memory but holds a stage through the softmax: 173 us against 13x us with 128 heads, 128
-//    sequences and 4096 shared tokens.)
-//  * One warp of the leader issues QK(g + 1) before PV(g), so the tensor cores work through the softmax of a
-//    tile. Shared-memory bandwidth bounds the rest: 240 KB of operands read, 138 KB loaded and 16 KB of P
-//    written per tile and CTA, 3,080 cycles at 128 bytes per cycle, against 2,176 of the MMAs.
+//    boxes); CTA h provides value dims [256h, 256h + 256) of both blocks. K's boxes cannot serve as V as well: an
+//    MMA takes its operand at the same offset in both CTAs, and there each holds its own block's tokens. So V is
+//    loaded on its own (from L2, where K has just put it) and K's boxes are free once Gemm1 has read them: K (9
+//    boxes), V (8) and Q (9) have one buffer each, refilled in groups behind the MMAs (139 KB a tile and CTA).
+//  * One thread of the leader issues QK(g + 1) before PV(g), so the tensor cores work through the softmax of a
+//    tile (two tiles ahead instead of one, with four score buffers: the same time).
+//  * What bounds it: a tile takes 2,480 cycles at 1.8 GHz against the 2,176 of its MMAs, and no role's waits
+//    are on the way any more; on calls of a few 100 us the power limit takes the clock to about 1.35 GHz. Beside that a
+//    call has about 5 us until its first tile (set-up, then 147 KB of Q and K a CTA at once), 5 us for its last
+//    piece's output, and as much again at each piece in between. Back to back, on 74 pairs: 64 sequences of 16 heads
+//    over 16,384 shared tokens 48 us (37 GFLOP); 128 of 128 heads over 4,096, 158 us with the merge (165 GFLOP,
+//    1,040 TFLOP/s); 33 of 64 heads over 65,536, 275 us (303 GFLOP, 1,100 TFLOP/s, where cuBLAS sustains 1,374).
 //  * Eight softmax warps, one thread per (row, 32 tokens); the four threads of a row agree on the running
 //    maximum through shared memory, O is rescaled only when it grows by more than 2^8 (P <= 2^8, exact
 //    in the fp32 sums). P is rounded to bf16 once (to nearest): an error of at most 2^-8 of each term, the
