@@ -21,20 +21,13 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 // Bounded waits without a suspend-time hint: with one, a warp was seen to wake up
 // to about a thousand cycles after its phase, which the short dependent steps of a pair kernel cannot hide.
 // Same contract as mbar_wait (false: *abort was set, or the bound passed and *abort is now set).
-__device__ __forceinline__ bool mbar_poll_once(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
-    return ok != 0;
-}
 __device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (mbar_poll_once(bar, parity)) return true;
+    if (mbar_test(bar, parity)) return true;
     const long long t0 = clock64();
     for (;;) {
 #pragma unroll 1
         for (int k = 0; k < 64; ++k)
-            if (mbar_poll_once(bar, parity)) return true;
+            if (mbar_test(bar, parity)) return true;
         if (*abort) return false;
         if (clock64() - t0 > kSpinCycles) {
             *abort = 1;
@@ -44,7 +37,7 @@ __device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volati
 }
 // For a whole converged warp: all lanes look at once (by lane 0 with a shuffle, a ready phase took 250 cycles).
 __device__ __forceinline__ bool warp_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (__all_sync(0xffffffffu, mbar_poll_once(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort));
 }
 
