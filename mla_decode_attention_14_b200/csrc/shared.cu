@@ -413,6 +413,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
             row_ok = w.pc.seq < 0 ? flat < p.total_rows : r < p.rows;
             vis = row_ok ? visible_keys(p.seqlens[seq], p.s_q, r / p.h_q, p.causal) : 0;
             vis = min(vis, min(w.pc.first_blk + 2 * w.pc.hi, w.pc.end_blk) * kBlk);
+            __syncwarp();
         }
         const int key0 = w.blk() * kBlk + blk * kBlk + 32 * th;
         wait(&sm.s_full[g & 1], (g >> 1) & 1);
@@ -423,7 +424,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
-        if (key0 + 32 > vis) {
+        if (__any_sync(0xffffffffu, key0 + 32 > vis)) {  // the same way for all lanes: a barrier of whole warps follows
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = key0 + j < vis ? v[j] : -INFINITY;
         }
@@ -488,6 +489,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(p_full);
+        __syncwarp();
 
         if (w.last()) {
             // the row's four sums, through the maxima's slots of the other parity (read before the barrier above)
@@ -509,8 +511,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
                 uint32_t o[16];
                 tmem_ld16(tmem + kTmemO + lane_off + 128 * th + 16 * c, o);
                 tmem_wait_ld();
-                if (!row_ok) continue;
-                if (whole) {
+                if (row_ok && whole) {
                     uint32_t wv[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -525,13 +526,14 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
                         reinterpret_cast<uint4 *>(dst)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
                         reinterpret_cast<uint4 *>(dst)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
                     }
-                } else {
+                } else if (row_ok) {
                     float *dst = p.o_part + (size_t)part_row * kDv + col + 16 * c;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
                     st_global_v8(dst, o);
                     st_global_v8(dst + 8, o + 8);
                 }
+                __syncwarp();  // a slice may be partly filled, and the next load is the whole warp's
             }
             if (row_ok && x == 0) {
                 if (whole) {
@@ -542,6 +544,7 @@ __device__ void softmax_role(Smem &sm, const SharedParams &p, Walker w, uint32_t
                     p.lse_part[part_row] = lse2;
                 }
             }
+            __syncwarp();
             tc_fence_before();  // ordered before the next tile's P, which lets Gemm2 overwrite O
         }
         w.advance(p);
