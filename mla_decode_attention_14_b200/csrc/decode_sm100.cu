@@ -969,10 +969,9 @@ __device__ void softmax_role(Smem &sm, const DecodeParams &p, const int32_t *met
                     const int col = 128 * c.th + 16 * q;
                     tmem_ld16(tmem + kTmemO + c.lane_off + col, v);
                     tmem_wait_ld();
-                    if (!c.row_ok) continue;
                     // 32-byte stores: each lane writes its own row, so a warp's store touches 32 rows and
                     // the number of stores, not their width, sets the epilogue's time
-                    if (whole) {
+                    if (c.row_ok && whole) {
                         uint32_t wv[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -987,13 +986,14 @@ __device__ void softmax_role(Smem &sm, const DecodeParams &p, const int32_t *met
                             reinterpret_cast<uint4 *>(dst)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
                             reinterpret_cast<uint4 *>(dst)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
                         }
-                    } else {
+                    } else if (c.row_ok) {
                         float *dst = p.o_part + ((size_t)a_slot * p.rows + c.r) * kDv + 256 * half + col;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * inv);
                         st_global_v8(dst, v);
                         st_global_v8(dst + 8, v + 8);
                     }
+                    __syncwarp();  // a slice may be partly filled, and the next load is the whole warp's
                 }
                 if (c.row_ok && half == 0 && c.th == 0) {
                     const float lse = empty ? -INFINITY : (m_ref + log2f(l_row)) * 0.69314718055994530942f;

@@ -128,6 +128,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
                     reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             }
+            __syncwarp();  // a slice may be partly filled, and the next load is the whole warp's
         }
     }
     tc_fence_before();

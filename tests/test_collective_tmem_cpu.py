@@ -35,7 +35,7 @@ def loops(text):
     return [b for b in out if not any(o is not b and o in b for o in out)]
 
 
-@pytest.mark.parametrize("path", [os.path.join(CSRC, f) for f in ("shared.cu",)], ids=os.path.basename)
+@pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(CSRC, "*.cu"))), ids=os.path.basename)
 def test_loops_around_collective_accesses_stay_converged(path):
     text = re.sub(r"//[^\n]*", "", open(path).read())
     for body in loops(text):
