@@ -297,7 +297,10 @@ int mla_head_gemm(const void *x, int64_t ldx, int64_t x_head_stride, const void 
  *   workspace      >= mla_shared_workspace_bytes(batch, s_q, h_q, shared_blocks, num_parts) bytes,
  *                  256-aligned; contents on entry are ignored. Calls that may overlap need one each.
  * All other arguments, outputs and status rules are those of mla_decode. Cache rows that some query row
- * sees must be finite; rows past every sequence's end may hold anything.
+ * sees must be finite; rows past every sequence's end may hold anything. A query row with a score of NaN or
+ * +inf gets NaN in out and lse (the lse of mla_decode is -inf for such a row), the others are not
+ * touched by it; a score of -inf weighs nothing, and a row with no other score is one without keys (out 0,
+ * lse -inf).
  * Precision: scores, softmax sums and outputs are accumulated in fp32 and the probabilities rounded to
  * bf16 (to nearest) for the second product, so that an output is off by at most 2^-8 (half a bf16 step) of
  * sum_j p_j |k_j| besides its own rounding; lse does not see that rounding. There is no range limit as in

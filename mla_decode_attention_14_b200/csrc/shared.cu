@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_kernel(const Shared
                 v[d][1] = src[1];
             }
             if (k0 == 0) {  // the weights of these pieces, while the outputs arrive
-                mx = fmaxf(m, ls);
+                mx = fmaxf(m, isnan(ls) ? 0.f : ls);  // a NaN piece weighs NaN; fmaxf would take it for one without keys
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 if (mx == -INFINITY) break;  // no key so far
