@@ -335,8 +335,9 @@ int mla_decode_shared(const void *q, const void *kv_cache, int64_t num_blocks, c
  * Large Language Models", section 3.2): pairs that make at least beta_fast turns over original_len positions
  * keep f_i, pairs with at most beta_slow turns take f_i / factor, with a linear ramp over i between.
  * `magnitude` is the caller's (1, or the scaled model's factor on queries and keys).
- *   turns[i] = round(2^64 * f_i / (2 pi)): the angle of position p is the fraction p * turns[i] mod 2^64 of
- *   a full turn, so every int32 position is reduced exactly.
+ *   turns[i] = the integer nearest to 2^64 * f_i / (2 pi), or one next to it: the angle of position p is the
+ *   fraction p * turns[i] mod 2^64 of a full turn, off by less than |p| * 2^-63 turns (2^-32 at the last int32
+ *   positions).
  * Returns MLA_ERR_INVALID_ARG unless base > 1, factor >= 1, original_len >= 0, beta_fast >= beta_slow > 0
  * and all are finite (magnitude in fp32).
  */

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 #include <mutex>
 
 #include <cuda.h>
@@ -647,22 +648,26 @@ int mla_rope_init(mla_rope *rope, double base, int interleaved, double factor, i
         !std::isfinite(beta_fast) || !std::isfinite((float)magnitude))
         return MLA_ERR_INVALID_ARG;
     constexpr int dim = MLA_D_QK - MLA_D_V;
-    const double pi = 3.14159265358979323846;
-    double low = 0.0, high = 0.0;
+    // In extended precision: 64 fixed-point bits hold more than a double's 53 (whose last place is 2^-56 of a turn here,
+    // or 2^-25 of one at position 2^31).
+    typedef long double Real;
+    static_assert(std::numeric_limits<Real>::digits >= 64, "turns need 64-bit significands");
+    const Real pi = 3.14159265358979323846264338327950288L;
+    Real low = 0.0L, high = 0.0L;
     if (original_len > 0) {  // the pairs that make beta_fast and beta_slow turns over original_len positions
-        const double ln = 2.0 * std::log(base);
-        low = std::floor(dim * std::log(original_len / (beta_fast * 2.0 * pi)) / ln);
-        high = std::ceil(dim * std::log(original_len / (beta_slow * 2.0 * pi)) / ln);
-        low = std::fmin(std::fmax(low, 0.0), dim - 1.0);
-        high = std::fmin(std::fmax(high, 0.0), dim - 1.0);
-        if (high <= low) high = low + 0.001;
+        const Real ln = 2.0L * std::log((Real)base);
+        low = std::floor(dim * std::log(original_len / (beta_fast * 2.0L * pi)) / ln);
+        high = std::ceil(dim * std::log(original_len / (beta_slow * 2.0L * pi)) / ln);
+        low = std::fmin(std::fmax(low, 0.0L), dim - 1.0L);
+        high = std::fmin(std::fmax(high, 0.0L), dim - 1.0L);
+        if (high <= low) high = low + 0.001L;
     }
     for (int i = 0; i < dim / 2; ++i) {
-        const double f = std::pow(base, -2.0 * i / dim);
+        const Real f = std::pow((Real)base, -2.0L * i / dim);
         // share of the interpolated frequency: 0 for fast pairs, 1 for slow ones; without original_len 1
-        const double ramp = original_len > 0 ? std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0) : 1.0;
-        const double turns = (f * (1.0 - ramp) + f / factor * ramp) / (2.0 * pi);  // per position, below 1 / 6
-        rope->turns[i] = (uint64_t)(std::ldexp(turns, 64) + 0.5);
+        const Real ramp = original_len > 0 ? std::fmin(std::fmax((i - low) / (high - low), 0.0L), 1.0L) : 1.0L;
+        const Real turns = (f * (1.0L - ramp) + f / factor * ramp) / (2.0L * pi);  // per position, below 1 / 6
+        rope->turns[i] = (uint64_t)(std::ldexp(turns, 64) + 0.5L);
     }
     rope->magnitude = (float)magnitude;
     rope->interleaved = interleaved;

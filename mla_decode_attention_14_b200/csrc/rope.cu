@@ -4,8 +4,8 @@
 // Pair i of the 64 dims (i = 0..31; interleaved: dims 2i, 2i + 1, half: dims i, i + 32) at position p is
 // turned by the angle p f_i and scaled by the magnitude a:
 //   y0 = a (x0 cos(p f_i) - x1 sin(p f_i)),  y1 = a (x0 sin(p f_i) + x1 cos(p f_i)).
-// The angle is reduced exactly: turn_i = round(2^64 f_i / 2 pi) comes from the host, and p * turn_i modulo
-// 2^64 is the fraction of a full turn in 64-bit fixed point, off by at most |p| 2^-65 turns, whatever the
+// The angle is reduced in integers: turn_i = 2^64 f_i / 2 pi comes from the host, within 1.5 units, and p * turn_i
+// modulo 2^64 is the fraction of a full turn in 64-bit fixed point, off by less than |p| 2^-63 turns, whatever the
 // position (an fp32 product would be off by radians at position 10^5). Its top 32 bits go to fp32 (an
 // error of at most 2^-26 turns), sine and cosine are taken there, and each result is rounded to bf16 once.
 #include <cuda_fp8.h>
