@@ -134,17 +134,17 @@ __global__ void __launch_bounds__(32 * kWarps, 16) append_kernel(const AppendPar
     // the rotary pair: one word (interleaved); half layout: the values of dims 2 (lane % 16), + 1 of this lane's half,
     // so that the row is read in whole words; the pair's other value comes from lane ^ 16
     const uint32_t two = reinterpret_cast<const uint32_t *>(src + kDv)[lane];
-    int b, t;  // sequence, place among its new tokens
+    int b, start;  // sequence, row of its first new token
     if (p.cu_new) {
         const int2 f = find_sequence(p.cu_new, p.batch, w, lane);
         b = f.x;
-        t = w - f.y;
+        start = f.y;
         if (b < 0) return;  // a row of no sequence
     } else {
         b = w / p.n_new;
-        t = w - b * p.n_new;
+        start = b * p.n_new;
     }
-    const int64_t at = (int64_t)max(p.seqlens[b], 0) + t;
+    const int64_t at = (int64_t)max(p.seqlens[b], 0) + ((int64_t)w - start);  // counts may start far below 0
     const int64_t bi = at / kBlk;
     const int32_t phys = bi < p.bt_stride ? p.block_table[(size_t)b * p.bt_stride + bi] : -1;
     if (phys < 0 || (int64_t)phys >= p.num_blocks) {

@@ -79,7 +79,10 @@ def test_bad_entries(fp8, packed, bad):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("cu", [[0, 3, 1, 3], [2, 1, 0, 3], [0, 0, 5, 3], [-7, 90, -90, 2], [3, 3, 3, 3], [0, 1 << 30, 2, 3],
-                                [-(1 << 31), (1 << 31) - 1, 0, (1 << 31) - 1]])
+                                [-(1 << 31), (1 << 31) - 1, 0, (1 << 31) - 1],
+                                # row 0 is token 2^31 of sequence 0: a place past 32 bits, and past its table
+                                [-(1 << 31), 1, 2, 3], [-(1 << 31), (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1],
+                                [2 - (1 << 31), 2, 2, 3]])
 def test_broken_counts(fp8, cu):
     """Counts that decrease, overlap or point outside: which token goes where is open, but only rows that some
     sequence's table and length address are written (what the last kept count leaves out is not)."""
