@@ -372,7 +372,8 @@ int mla_rope_q(const void *x, int64_t ldx, int64_t x_head_stride, void *y, int64
  *     latent: x * rsqrt(mean(x^2) + eps) * norm_weight over its 512 latent dims (norm_weight NULL: x)
  *     rotary: the 64 rotary dims turned to the token's position (see mla_rope)
  * each rounded once to the cache's type (mla_append_kv / mla_append_kv_fp8's rules for rows, types and
- * kv_scale).
+ * kv_scale). The norm holds for latents of any finite size (sums in fp32, in 64 bits where those would leave
+ * its range); NaN and Inf go through the formula.
  *   cu_new      NULL: tokens = batch * n_new, token t of sequence b is row b * n_new + t. Otherwise int32
  *               [batch + 1], non-decreasing: packed sequences, rows [cu_new[b], cu_new[b+1]) are those of
  *               sequence b (none, if equal), n_new is not used, and rows outside [cu_new[0], cu_new[batch])

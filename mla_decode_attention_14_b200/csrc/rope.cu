@@ -115,6 +115,33 @@ __device__ __forceinline__ int2 find_sequence(const int32_t *cu, int batch, int 
     return i < end && start <= i ? make_int2(lo, start) : make_int2(-1, 0);
 }
 
+// The normed latent of a row whose squares leave fp32 (a mean past 2^127, or below 2^-100, where squares lose places
+// to fp32's smallest step 2^-149): sum and root in 64 bits, where every bf16 value's square fits. A whole path of its
+// own, so that the usual one keeps no registers for it.
+template <bool F8>
+__device__ __noinline__ void far_latent(const __nv_bfloat16 *x, int64_t ld, const __nv_bfloat16 *weight, float eps,
+                                        float inv_scale, uint8_t *dst) {
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *src = x + (int64_t)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * ld;
+    double ss = 0.0;
+#pragma unroll 1
+    for (int i = lane; i < kDv; i += 32) {
+        const double x = __bfloat162float(src[i]);
+        ss = fma(x, x, ss);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const double rn = 1.0 / sqrt(ss / kDv + eps);
+#pragma unroll 1
+    for (int i = lane; i < kDv; i += 32) {
+        const float y = (float)(__bfloat162float(src[i]) * rn) * __bfloat162float(weight[i]);
+        if constexpr (F8)
+            dst[i] = (uint8_t)__nv_cvt_float_to_fp8(y * inv_scale, __NV_SATFINITE, __NV_E4M3);
+        else
+            reinterpret_cast<__nv_bfloat16 *>(dst)[i] = __float2bfloat16_rn(y);
+    }
+}
+
 // New tokens into the cache: bounded by bytes (1152 in, 1152 or 640 out per token) for prompts, by
 // latency for a decode step. One warp per token: a lane holds two 16-byte chunks of the latent and one rotary
 // pair; the sum of squares is a warp reduction in fp32, and the row is read and written once.
@@ -168,6 +195,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16) append_kernel(const AppendPar
         rotated = pack_bf16(lo_f(two) * c0.x + sg * (lo_f(other) * c0.y), hi_f(two) * c1.x + sg * (hi_f(other) * c1.y));
     }
 
+    uint8_t *dst = p.kv + row * (int64_t)(F8 ? kF8Record : kDqk * 2);
     const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
     float v[16];
 #pragma unroll
@@ -184,14 +212,19 @@ __global__ void __launch_bounds__(32 * kWarps, 16) append_kernel(const AppendPar
         for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rn = rsqrtf(ss * (1.f / kDv) + p.eps);
+        const float ms = ss * (1.f / kDv) + p.eps;
+        if (!(ms >= 0x1p-100f && ms <= 0x1p127f)) {  // the same way for all lanes
+            reinterpret_cast<uint32_t *>(dst + (F8 ? kDv : kDv * 2))[lane] = rotated;
+            far_latent<F8>(p.x, p.ld, p.weight, p.eps, p.inv_scale, dst);
+            return;
+        }
+        const float rn = rsqrtf(ms);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[2 * i] = v[2 * i] * rn * lo_f(ww[i]);
             v[2 * i + 1] = v[2 * i + 1] * rn * hi_f(ww[i]);
         }
     }
-    uint8_t *dst = p.kv + row * (int64_t)(F8 ? kF8Record : kDqk * 2);
     if constexpr (F8) {
         uint32_t o[4];
 #pragma unroll
