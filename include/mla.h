@@ -303,8 +303,10 @@ int mla_head_gemm(const void *x, int64_t ldx, int64_t x_head_stride, const void 
  * lse -inf).
  * Precision: scores, softmax sums and outputs are accumulated in fp32 and the probabilities rounded to
  * bf16 (to nearest) for the second product, so that an output is off by at most 2^-8 (half a bf16 step) of
- * sum_j p_j |k_j| besides its own rounding; lse does not see that rounding. There is no range limit as in
- * mla_decode. Results do not depend on timing: no atomics, a fixed order of sums for given metadata.
+ * sum_j p_j |k_j| besides its own rounding; lse does not see that rounding. mla_decode holds them in two bf16
+ * terms (2^-14): a batch that moves here gives that up (measured against 64 bits, relative over a whole output:
+ * 1.8e-3 to 2.0e-3 where its bf16 rounding alone is 1.65e-3). There is no range limit as in mla_decode, but scores
+ * are fp32: one may be off by 2^-16 of scale * sum_i |q_i k_i|. Results do not depend on timing: no atomics, a fixed order of sums for given metadata.
  * Two launches on `stream`; allocates nothing.
  */
 int64_t mla_shared_units(int batch, int s_q, int h_q, int shared_blocks);  /* 0 for invalid sizes; host only */

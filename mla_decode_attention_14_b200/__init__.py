@@ -476,7 +476,7 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, shared_table: torch.T
     ``shared_table`` int32 ``[shared_blocks]``: the prefix's blocks; row b of ``block_table`` holds sequence b's
     blocks from entry ``shared_blocks`` on (earlier entries are not read); ``seqlens`` are whole lengths.
     Returns ``(out bf16 [b, s_q, h_q, 512], lse fp32 [b, h_q, s_q])``, as :func:`decode` with tables that
-    all begin with ``shared_table``. Tensors made here belong to ``stream`` (the current one by default).
+    all begin with ``shared_table``, but for the probabilities: one bf16 term where :func:`decode` has two. Tensors made here belong to ``stream`` (the current one by default).
     """
     i = q.get_device()
     if not (i >= 0 and _is(q, torch.bfloat16, i, 4)):

@@ -145,10 +145,13 @@ __device__ __noinline__ void far_latent(const __nv_bfloat16 *x, int64_t ld, cons
 // New tokens into the cache: bounded by bytes (1152 in, 1152 or 640 out per token) for prompts, by
 // latency for a decode step. One warp per token: a lane holds two 16-byte chunks of the latent and one rotary
 // pair; the sum of squares is a warp reduction in fp32, and the row is read and written once.
-// The input is dead once read, and a prompt's rows are not read back before much else has been: loads and latent
-// stores are hinted evict-first. 36,800 packed tokens into a bf16 cache, cold: 18.6 us (4.5 TB/s); blocks of 8 and 16
+// The input is dead once read, and a prompt's rows are not read back before much else has been: loads, and the latent
+// stores into a bf16 cache, are hinted evict-first (an fp8 cache's are plain). A decode step's rows, which the attention
+// reads right behind, take the same path: the hint orders evictions and forces none, and at worst those few rows (147 KB
+// for 128 tokens) come from HBM again. 36,800 packed tokens into a bf16 cache, cold: 18.6 us (4.5 TB/s); blocks of 8 and 16
 // warps 18.9 and 20.0, without the hints 19.5, with a plain launch 20.5; the registers of 48 instead of 64 warps
-// an SM cost 0.6 us, two or four tokens a warp with all loads ahead 4 and 9 (no writes beside the reads).
+// an SM cost 0.6 us (at its 32 registers the kernel spills 16 to 28 bytes a thread: 24 MB of stores and as much of
+// loads in L1 over that call), two or four tokens a warp with all loads ahead 4 and 9 (no writes beside the reads).
 template <bool F8, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps, 16) append_kernel(const AppendParams p, const __grid_constant__ mla_rope rope) {
     sm100::wait_for_previous_kernel();
